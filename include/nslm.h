@@ -97,6 +97,26 @@ typedef struct {
     int32_t P;               /* 3, 4 or NSLM_P3C5 */
 } nslm_seed_matrix;
 
+/* One matrix in 4 bits with a scale, and optionally an offset, for each group
+ * of weights along K: the affine layout in which seed packs hold their
+ * non-expert weights ("K2-Horizon-MoVA-36B-A4B -- NanoSeedLM p4mx-q4v", "This
+ * upload").  Row-major, little-endian; ng = K / group:
+ *   q       uint32 [N][K/8]  weight 8j+i of a row in bits 4i..4i+3 of word j,
+ *                            unsigned, 0..15
+ *   scales  bf16   [N][ng]
+ *   biases  bf16   [N][ng], or NULL
+ * W[i][k] = scales[i][k / group] * q + biases[i][k / group], and without
+ * biases W[i][k] = scales[i][k / group] * (q - 8).  group is 32, 64 or 128;
+ * K is a multiple of it. */
+typedef struct {
+    const uint32_t *q;
+    const uint16_t *scales;
+    const uint16_t *biases;  /* NULL: symmetric */
+    int32_t N;
+    int32_t K;
+    int32_t group;
+} nslm_q4_matrix;
+
 /* One MoE layer: gate and up are [E * inter][hidden], down is [E * hidden][inter]. */
 typedef struct {
     nslm_seed_matrix gate;
@@ -110,6 +130,7 @@ typedef struct {
 #define NSLM_OP_MOE_FFN 2
 #define NSLM_OP_MOE_STACK 3
 #define NSLM_OP_MOE_FFN_HYBRID 4  /* E = E3 + E4 */
+#define NSLM_OP_MOE_BALANCE 5     /* nslm_moe_balance: T, E and k */
 
 /* Bytes of workspace an operation needs (0 if none).  T = tokens, E =
  * experts, hidden/inter = FFN sizes, k = experts per token, L = layers (only
@@ -141,6 +162,19 @@ int32_t nslm_seed_gemv(const nslm_seed_matrix *W, const uint16_t *x_bf16, int32_
 int32_t nslm_seed_gemv_flags(const nslm_seed_matrix *W, const uint16_t *x_bf16, int32_t M,
                              float *y, uint32_t flags, nslm_stream_t stream);
 
+/* GEMV from 4-bit weights, for the projections that stay outside the seed
+ * format (router, output head, attention):
+ *   y[m][i] = sum_k W[i][k] * x[m][k],  m < M, i < N.
+ * x: bf16 [M][K]; y: fp32 [M][N]; 1 <= M <= 8; M * K <= 65536 (the activations
+ * stay in shared memory).  Products are exact, sums are held in fp32; the
+ * weights are never rounded.  Finite x.  flags: 0 or NSLM_GEMV_FIELDS_READY,
+ * with the meaning of nslm_seed_gemv_flags (no kernel enqueued earlier on
+ * `stream` writes W's q, scales or biases); other bits return NSLM_ERR_ARG.
+ * The result does not depend on timing (no atomics).  One launch, no
+ * workspace.  y must not overlap any input. */
+int32_t nslm_q4_gemv(const nslm_q4_matrix *W, const uint16_t *x_bf16, int32_t M, float *y,
+                     uint32_t flags, nslm_stream_t stream);
+
 /* Grouped seed GEMM over stacked experts, the batched (prefill) product of
  * "Qwen3.8-Flash-Next" prompt processing ("The prompt time ... the grouped
  * expert GEMMs", NanoSeedLM documentation index, Results).
@@ -164,6 +198,82 @@ int32_t nslm_seed_grouped_gemm(const nslm_seed_matrix *W, int32_t E, const uint1
  * k <= E <= 1024.  ("Why K2-Horizon-MoVA": 100 routed experts, top 8.) */
 int32_t nslm_moe_route_topk(const float *logits, int32_t T, int32_t E, int32_t k,
                             int32_t *ids, float *w, nslm_stream_t stream);
+
+/* How evenly a router loads its experts: the experts' counts and the balance
+ * loss.  With n the number of tokens that count (mask[t] != 0; all T where
+ * mask is NULL), c_e the number of their routed pairs ids[t][q] == e, and
+ * p_t the softmax of all E logits of token t:
+ *   mean_p[e] = 1/n sum_t p_t[e]
+ *   loss      = coef * E * sum_e c_e / (k n) * mean_p[e]
+ * (even counts give coef).  logits: fp32 [T][E]; ids: int32 [T][k], as
+ * nslm_moe_route_topk writes them (an id outside [0, E) counts nowhere; one
+ * listed twice counts twice); mask: uint8 [T] or NULL.  Logits and ids of
+ * tokens that do not count are not looked at.  A logit of -inf has probability
+ * zero; a token whose logits are all -inf counts but adds nothing to mean_p.
+ * Written, all on the device: counts int32 [E + 1], c_e and then n; offsets
+ * int32 [E + 1] or NULL, the counts' running sum from 0, as
+ * nslm_seed_grouped_gemm takes them for rows grouped by expert; mean_p fp32
+ * [E] or NULL; loss fp32 [1].  n = 0 (or T = 0) gives zeros.
+ * 1 <= k <= 8, k <= E <= 1024.  Sums are taken in a fixed order: equal calls
+ * give equal bits.  T <= 1024 takes one launch and no workspace (ws may be
+ * NULL), larger T two.  Workspace:
+ * nslm_workspace_bytes(NSLM_OP_MOE_BALANCE, T, E, 0, 0, k, 0). */
+int32_t nslm_moe_balance(const float *logits, const int32_t *ids, const uint8_t *mask, int32_t T,
+                         int32_t E, int32_t k, float coef, int32_t *counts, int32_t *offsets,
+                         float *mean_p, float *loss, void *ws, size_t ws_bytes, nslm_stream_t stream);
+
+/* The gradient of nslm_moe_balance's loss with respect to the logits (the
+ * counts are constants: the choice of experts has no gradient):
+ *   dlogits[t][e] = dloss * coef * E / n * p_t[e] * (f_e - sum_j f_j p_t[j]),
+ *   f_e = c_e / (k n)
+ * and zeros in the rows of tokens that do not count.  counts: int32 [E + 1] as
+ * nslm_moe_balance wrote them (a data-parallel caller may sum c_e and n over
+ * its ranks first: the gradient is then that of the whole batch's loss);
+ * dloss: fp32 [1], device, the gradient that arrives at the loss, or NULL for
+ * 1; dlogits: fp32 [T][E], written whole; it may be logits itself.
+ * One launch, no workspace. */
+int32_t nslm_moe_balance_grad(const float *logits, const int32_t *counts, const uint8_t *mask,
+                              int32_t T, int32_t E, int32_t k, float coef, const float *dloss,
+                              float *dlogits, nslm_stream_t stream);
+
+/* Element types. */
+#define NSLM_TYPE_F32 0
+#define NSLM_TYPE_BF16 1
+
+/* Per-row settings of nslm_sample: HOST struct of DEVICE arrays of B values;
+ * a NULL array leaves its filter out (temperature: 1). */
+typedef struct {
+    const float *temperature; /* > 0; anything else, NaN too, takes the most likely token */
+    const int32_t *top_k;     /* <= 0 or >= V: off */
+    const float *top_p;       /* >= 1 or NaN: off; <= 0 keeps the most likely token */
+    const float *min_p;       /* <= 0 or NaN: off; >= 1 keeps the tokens as likely as the first */
+} nslm_sample_params;
+
+/* Draws one token a row from logits (an output head's, such as nslm_q4_gemv
+ * writes them) at given random numbers u.  For one row, with m its largest
+ * logit and w_i = exp((logit_i - m) / temperature), tokens in descending order
+ * of their logits, ties by the lower index:
+ *   1. top-k keeps the first top_k tokens;
+ *   2. top-p keeps, of these, the fewest first tokens whose w sum to at least
+ *      top_p times the sum over 1.'s;
+ *   3. min-p keeps, of these, those with w_i >= min_p;
+ *   the first token always stays.
+ *   token = the lowest index i for which the sum of the kept w_j, j <= i,
+ *   exceeds u times the sum Z of all kept w;   prob = w_token / Z.
+ * So equal u give equal tokens on every call: w is taken in fp64 and summed as
+ * 64-bit fixed point with 44 bits behind the point, whose sums are exact and
+ * know no order; tokens with w < 2^-45 are not drawn.  u below 0 (or NaN)
+ * counts as 0, u from 1 on as just below 1.  A temperature that is not
+ * positive takes the first token, with prob 1.
+ * A logit of -inf or NaN is never drawn; where +inf occurs, only those tokens
+ * are left, equally likely.  A row with nothing left gives token -1, prob 0.
+ * logits: [B] rows of V values of type `type`, `ld` >= V elements apart, only
+ * read; u: fp32 [B]; token: int32 [B]; prob: fp32 [B] or NULL; params NULL:
+ * plain sampling at temperature 1.  B >= 0, 1 <= V <= 262144.  One launch, no
+ * workspace. */
+int32_t nslm_sample(const void *logits, int32_t type, int32_t B, int32_t V, int64_t ld,
+                    const nslm_sample_params *params, const float *u, int32_t *token, float *prob,
+                    nslm_stream_t stream);
 
 /* Routed expert FFN for T tokens ("Why K2-Horizon-MoVA": routed FFN experts,
  * top 8; gate and up projections, SiLU, down projection):

@@ -43,6 +43,9 @@ int32_t check_matrix(const nslm_seed_matrix *W);
 // of nslm_moe_seed_ffn_static on the current device.
 int32_t static_scratch_status_word(const int32_t **out);
 
+// Workspace of nslm_moe_balance.
+size_t balance_ws_bytes(int32_t T, int32_t E);
+
 // Work layout of one seed matrix product: a CTA covers R rows x C chunks of
 // 8 blocks (64 weights); C = ceil(nb / 8).
 struct ChunkLayout {

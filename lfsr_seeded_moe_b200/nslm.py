@@ -39,6 +39,10 @@ NSLM_OP_GROUPED_GEMM = 1
 NSLM_OP_MOE_FFN = 2
 NSLM_OP_MOE_STACK = 3
 NSLM_OP_MOE_FFN_HYBRID = 4
+NSLM_OP_MOE_BALANCE = 5
+
+NSLM_TYPE_F32 = 0
+NSLM_TYPE_BF16 = 1
 
 
 class NslmError(RuntimeError):
@@ -63,6 +67,26 @@ class nslm_moe_layer(ctypes.Structure):
     _fields_ = [("gate", nslm_seed_matrix), ("up", nslm_seed_matrix), ("down", nslm_seed_matrix)]
 
 
+class nslm_q4_matrix(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("biases", ctypes.c_void_p),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+    ]
+
+
+class nslm_sample_params(ctypes.Structure):
+    _fields_ = [
+        ("temperature", ctypes.c_void_p),
+        ("top_k", ctypes.c_void_p),
+        ("top_p", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -74,8 +98,12 @@ def _load():
         "nslm_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32, i32]),
         "nslm_seed_gemv": (i32, [mp, vp, i32, vp, vp, sz, vp]),
         "nslm_seed_gemv_flags": (i32, [mp, vp, i32, vp, ctypes.c_uint32, vp]),
+        "nslm_q4_gemv": (i32, [ctypes.POINTER(nslm_q4_matrix), vp, i32, vp, ctypes.c_uint32, vp]),
         "nslm_seed_grouped_gemm": (i32, [mp, i32, vp, vp, i32, vp, vp, sz, vp]),
         "nslm_moe_route_topk": (i32, [vp, i32, i32, i32, vp, vp, vp]),
+        "nslm_moe_balance": (i32, [vp, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]),
+        "nslm_moe_balance_grad": (i32, [vp, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp]),
+        "nslm_sample": (i32, [vp, i32, i32, i32, ctypes.c_int64, ctypes.POINTER(nslm_sample_params), vp, vp, vp, vp]),
         "nslm_moe_seed_ffn": (i32, [mp, mp, mp, i32, vp, vp, vp, i32, i32, vp, vp, sz, vp]),
         "nslm_moe_seed_ffn_hybrid": (i32, [ctypes.POINTER(nslm_moe_layer), i32, ctypes.POINTER(nslm_moe_layer), i32,
                                            vp, vp, vp, i32, i32, vp, vp, sz, vp]),
@@ -185,6 +213,16 @@ def nslm_seed_gemv_flags(W, x_bf16, M: int, y, flags: int = 0, stream=None) -> N
                                                               int(flags), _s(stream)))
 
 
+def q4_matrix(q, scales, biases, group: int) -> nslm_q4_matrix:
+    """Marshal 4-bit weights: q int32 [N][K/8], scales and biases (or None) bf16 [N][K/group]."""
+    return nslm_q4_matrix(_p(q), _p(scales), _p(biases), int(q.shape[0]), int(q.shape[1]) * 8, int(group))
+
+
+def nslm_q4_gemv(W, x_bf16, M: int, y, flags: int = 0, stream=None) -> None:
+    """W: an nslm_q4_matrix (see q4_matrix)."""
+    _check("nslm_q4_gemv", _lib.nslm_q4_gemv(ctypes.byref(W), _p(x_bf16), M, _p(y), int(flags), _s(stream)))
+
+
 def nslm_seed_grouped_gemm(W, E: int, x_bf16, offsets, R: int, y, ws=None, ws_bytes: int = 0,
                            stream=None) -> None:
     _check("nslm_seed_grouped_gemm",
@@ -195,6 +233,32 @@ def nslm_seed_grouped_gemm(W, E: int, x_bf16, offsets, R: int, y, ws=None, ws_by
 def nslm_moe_route_topk(logits, T: int, E: int, k: int, ids, w, stream=None) -> None:
     _check("nslm_moe_route_topk",
            _lib.nslm_moe_route_topk(_p(logits), T, E, k, _p(ids), _p(w), _s(stream)))
+
+
+def nslm_moe_balance(logits, ids, mask, T: int, E: int, k: int, coef: float, counts, offsets, mean_p, loss,
+                     ws=None, ws_bytes: int = 0, stream=None) -> None:
+    _check("nslm_moe_balance",
+           _lib.nslm_moe_balance(_p(logits), _p(ids), _p(mask), T, E, k, coef, _p(counts), _p(offsets), _p(mean_p),
+                                 _p(loss), _p(ws), ws_bytes, _s(stream)))
+
+
+def nslm_moe_balance_grad(logits, counts, mask, T: int, E: int, k: int, coef: float, dloss, dlogits,
+                          stream=None) -> None:
+    _check("nslm_moe_balance_grad",
+           _lib.nslm_moe_balance_grad(_p(logits), _p(counts), _p(mask), T, E, k, coef, _p(dloss), _p(dlogits),
+                                      _s(stream)))
+
+
+def sample_params(temperature=None, top_k=None, top_p=None, min_p=None) -> nslm_sample_params:
+    """Marshal the per-row settings of nslm_sample (tensors or None); the caller keeps the tensors."""
+    return nslm_sample_params(_p(temperature), _p(top_k), _p(top_p), _p(min_p))
+
+
+def nslm_sample(logits, type: int, B: int, V: int, ld: int, params, u, token, prob=None, stream=None) -> None:
+    """params: an nslm_sample_params (see sample_params) or None."""
+    _check("nslm_sample",
+           _lib.nslm_sample(_p(logits), type, B, V, ld, None if params is None else ctypes.byref(params), _p(u),
+                            _p(token), _p(prob), _s(stream)))
 
 
 def nslm_moe_seed_ffn(gate, up, down, E: int, x_bf16, ids, w, T: int, k: int, y, ws=None,
