@@ -107,7 +107,7 @@ typedef struct {
  *   biases  bf16   [N][ng], or NULL
  * W[i][k] = scales[i][k / group] * q + biases[i][k / group], and without
  * biases W[i][k] = scales[i][k / group] * (q - 8).  group is 32, 64 or 128;
- * K is a multiple of it. */
+ * K is a multiple of it; N is at most 2^30. */
 typedef struct {
     const uint32_t *q;
     const uint16_t *scales;
@@ -165,8 +165,8 @@ int32_t nslm_seed_gemv_flags(const nslm_seed_matrix *W, const uint16_t *x_bf16, 
 /* GEMV from 4-bit weights, for the projections that stay outside the seed
  * format (router, output head, attention):
  *   y[m][i] = sum_k W[i][k] * x[m][k],  m < M, i < N.
- * x: bf16 [M][K]; y: fp32 [M][N]; 1 <= M <= 8; M * K <= 65536 (the activations
- * stay in shared memory).  Products are exact, sums are held in fp32; the
+ * x: bf16 [M][K]; y: fp32 [M][N]; 1 <= M <= 8; M, rounded up to 1, 2,
+ * 4 or 8, times K is at most 65536 (the activations stay in shared memory).  Products are exact, sums are held in fp32; the
  * weights are never rounded.  Finite x.  flags: 0 or NSLM_GEMV_FIELDS_READY,
  * with the meaning of nslm_seed_gemv_flags (no kernel enqueued earlier on
  * `stream` writes W's q, scales or biases); other bits return NSLM_ERR_ARG.

@@ -2,6 +2,8 @@
 // with a scale (and an offset) for each group along K.
 #include <algorithm>
 
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 
 namespace nslm {
@@ -12,44 +14,370 @@ constexpr int kMaxMK = 65536;  // bf16 activations of one call that stay in shar
 
 __device__ __forceinline__ float bf16_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
-// One warp per row; a lane takes every 32nd word of 8 weights.
-template <int M>
-__global__ void __launch_bounds__(256) q4_gemv_kernel(const nslm_q4_matrix W, const uint16_t *__restrict__ x,
-                                                      float *__restrict__ y) {
+// A tile is 16 rows.  kw warps of a CTA share a tile, each with a range of the
+// groups along K, and add their sums in shared memory at its end; a CTA has
+// WARPS / kw tiles at a time and walks over the rows.  Weights come by cp.async
+// into a ring of STAGES x (16 rows x 256 weights) of each warp's own, which
+// runs ahead across tiles, so no load waits for the sums or the barrier.
+//
+// The product runs on mma.sync m16n8k16 with the weights as A (q - 8, exact in
+// bf16, straight from the packed words to the fragment's registers) and the
+// vectors as B: with at most 8 vectors the tensor cores' 128-row form would
+// spend its time on building operands, and a CUDA-core product would be bound
+// by its fp32 multiply-adds from two vectors on.  A word holds weights 0..7 of
+// a row; the pairs (0,4), (1,5), (2,6), (3,7) are what a mask takes out of it
+// at once, so these are the fragment's pairs, and the staged activations are in
+// the same order.  Each group gets an accumulator of its own, multiplied by the
+// scale in fp32; products are exact, so nothing of a weight is rounded.  The
+// rest of an affine weight, (b + 8 s) times the group's sum of x, is a product
+// over the groups with b and s as they are stored (bf16) and the sum in three
+// bf16 parts (24 bits), 6 mma for every 16 groups.
+
+constexpr int kTile = 16;
+constexpr int kStageK = 256;             // weights of a row in a stage
+constexpr int kRow = kStageK / 2;        // and their bytes
+constexpr int kStage = kTile * kRow;
+constexpr int kZero = 8 * 4 * 16 * 4;    // bytes of zeros that lanes without a vector read in a stage
+
+struct Q4Params {
+  nslm_q4_matrix W;
+  const uint16_t *x;
+  float *y;
+  int32_t M, NG;    // NG: groups of a row
+  int32_t kw;       // warps that share a tile
+  int32_t steps;    // tiles / (WARPS / kw), rounded up
+  int32_t pos;      // group positions of a vector's sums: 16 ceil(most groups of a warp / 16) for each of kw
+  bool ready;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The bf16 pair (w_i - 8, w_{i+4} - 8) of a word: 0x4300 | q is 128 + q.
+template <int I>
+__device__ __forceinline__ uint32_t pair_of(uint32_t v) {
+  uint32_t p, r;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(p) : "r"(v >> (4 * I)), "r"(0x43004300u));
+  asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(0x43084308u));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+template <int WORDS>
+__device__ __forceinline__ void lds_words(uint32_t (&a)[WORDS], uint32_t at) {
+  if constexpr (WORDS == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a[0]) : "r"(at) : "memory");
+  if constexpr (WORDS == 2) asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(a[0]), "=r"(a[1]) : "r"(at) : "memory");
+  if constexpr (WORDS == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// MP: vectors in shared memory, M rounded up to 1, 2, 4 or 8 (zeros behind the last).
+template <int G, int MP, int WARPS, int STAGES, bool AFFINE>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel(const Q4Params p) {
+  constexpr int kWords = G / 32;       // words of a row and group for each of 4 lanes
+  constexpr int kGps = kStageK / G;    // groups of a stage
+  constexpr int kSpb = 16 / kGps;      // stages of a batch of 16 groups
+  // The 16-byte chunks of a stage's row change places by the row, so that the
+  // rows that one phase of a shared-memory load reads lie in different banks.
+  constexpr int kFlip = G / 2;         // in units of a group's bytes
+  constexpr int kFlips = kRow / kFlip; // 8, 4 or 2
+  extern __shared__ uint4 smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int M = p.M, K = p.W.K, N = p.W.N, NG = p.NG;
+  uint4 *xs = smem + kZero / 16;  // [K / 32][MP][4], behind the zeros
+  uint16_t *sx = reinterpret_cast<uint16_t *>(xs + (size_t)MP * K / 8);  // [3][MP][pos + 8]
+  const int sx_row = p.pos + 8;
+  uint8_t *rings = reinterpret_cast<uint8_t *>(sx) + (AFFINE ? 6 * MP * sx_row : 0);
+  float *red = reinterpret_cast<float *>(rings + WARPS * STAGES * kStage);  // [2][WARPS][8][16]
+  const uint32_t ring = smem_addr(rings) + warp * STAGES * kStage;
+
+  const int sub = warp / p.kw, kp = warp - sub * p.kw, tps = WARPS / p.kw;
+  const int g0 = kp * NG / p.kw, g1 = (kp + 1) * NG / p.kw;
+  const int nst = (g1 - g0 + kGps - 1) / kGps;  // stages of a tile
+
+  // the load side: which stage comes next, and its two row pointers
+  int l_step = blockIdx.x, l_st = 0, l_left = 0;
+  uint32_t l_slot = 0;
+  const uint8_t *src0 = nullptr, *src1 = nullptr;
+  auto rows_of = [&]() {
+    const int row = (l_step * tps + sub) * kTile + g;
+    const size_t pitch = (size_t)K / 2;
+    const uint8_t *base = reinterpret_cast<const uint8_t *>(p.W.q) + (size_t)g0 * (G / 2) + t * 16;
+    src0 = base + (size_t)min(row, N - 1) * pitch;
+    src1 = base + (size_t)min(row + 8, N - 1) * pitch;
+    l_left = (g1 - g0) * G - t * 32;
+    l_st = nst;
+  };
+  // chunks t and t + 4 of rows g and g + 8 are this lane's to copy
+  const uint32_t dst0 = ring + g * kRow + ((t * 16) ^ ((g % kFlips) * kFlip));
+  const uint32_t dst1 = ring + g * kRow + ((t * 16 + 64) ^ ((g % kFlips) * kFlip));
+  if (l_step < p.steps) rows_of();
+  auto load_stage = [&]() {
+    if (l_st > 0) {
+      if (l_left > 0) {
+        copy16(dst0 + l_slot, src0);
+        copy16(dst0 + l_slot + 8 * kRow, src1);
+      }
+      if (l_left > 128) {
+        copy16(dst1 + l_slot, src0 + 64);
+        copy16(dst1 + l_slot + 8 * kRow, src1 + 64);
+      }
+      src0 += kRow, src1 += kRow;
+      l_left -= kStageK;
+      l_slot = l_slot == (STAGES - 1) * kStage ? 0 : l_slot + kStage;
+      if (--l_st == 0) {
+        l_step += gridDim.x;
+        if (l_step < p.steps) rows_of();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // scales and offsets of 16 groups in the A fragment's layout, one batch ahead
+  uint32_t sc[4], of[4], sc_next[4], of_next[4];
+  const bool paired = ((NG | g0 | (g1 - g0)) & 1) == 0;  // two groups' values lie in one aligned word
+  auto load_scales = [&](int step, int b) {
+    const int row = (step * tps + sub) * kTile + g;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int gi = g0 + b * 16 + 2 * t + 8 * (r >> 1);
+      const size_t at = (size_t)min(row + 8 * (r & 1), N - 1) * NG + gi;
+      sc_next[r] = of_next[r] = 0;
+      if (gi - 2 * t >= g1) continue;
+      if (paired) {
+        if (gi < g1) {
+          sc_next[r] = __ldg(reinterpret_cast<const uint32_t *>(p.W.scales + at));
+          if (AFFINE) of_next[r] = __ldg(reinterpret_cast<const uint32_t *>(p.W.biases + at));
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (gi + h < g1) {
+            sc_next[r] |= (uint32_t)__ldg(p.W.scales + at + h) << (16 * h);
+            if (AFFINE) of_next[r] |= (uint32_t)__ldg(p.W.biases + at + h) << (16 * h);
+          }
+      }
+    }
+  };
+  auto prologue = [&]() {
+    for (int i = 0; i < STAGES - 1; ++i) load_stage();
+    if (blockIdx.x < p.steps) load_scales(blockIdx.x, 0);
+  };
+
+  if (p.ready) prologue();
+  for (int i = tid; i < kZero / 16; i += WARPS * 32) smem[i] = make_uint4(0, 0, 0, 0);
+  if (AFFINE) {
+    for (int i = tid; i < 3 * MP * sx_row / 2; i += WARPS * 32) reinterpret_cast<uint32_t *>(sx)[i] = 0;
+    __syncthreads();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= W.N) return;
-  const int nw = W.K / 8, ng = W.K / W.group;
-  float acc[M] = {};
-  for (int j = lane; j < nw; j += 32) {
-    const uint32_t v = W.q[(size_t)row * nw + j];
-    const int g = 8 * j / W.group;
-    const float s = bf16_f32(W.scales[(size_t)row * ng + g]);
-    const float b = W.biases ? bf16_f32(W.biases[(size_t)row * ng + g]) : -8.f * s;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!p.ready) prologue();
+
+  // activations: word wi of a group is what lane wi / kWords multiplies in step wi % kWords
+  for (int i = tid; i < MP * K / 8; i += WARPS * 32) {
+    const int m = i / (K / 8), w = i - m * (K / 8), gi = w / (G / 8), wi = w - gi * (G / 8);
+    const uint4 v = m < M ? __ldg(reinterpret_cast<const uint4 *>(p.x) + i) : make_uint4(0, 0, 0, 0);
+    const uint4 q = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+    xs[((size_t)(gi * kWords + wi % kWords) * MP + m) * 4 + wi / kWords] = q;
+    if (AFFINE) {
+      float s = 0.f;
+      const uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float w = fmaf(s, (float)((v >> (4 * i)) & 15u), b);
+      for (int j = 0; j < 4; ++j) s += bf16_f32(h[j] & 0xffffu) + __uint_as_float(h[j] & 0xffff0000u);
+      // G / 8 neighbouring lanes hold a group; groups do not straddle the end
+      const int left = MP * K / 8 - (i - lane);
+      const uint32_t mask = left >= 32 ? 0xffffffffu : (1u << left) - 1;
 #pragma unroll
-      for (int m = 0; m < M; ++m) acc[m] = fmaf(w, bf16_f32(x[(size_t)m * W.K + 8 * j + i]), acc[m]);
+      for (int o = 1; o < G / 8; o <<= 1) s += __shfl_xor_sync(mask, s, o);
+      if (wi == 0) {
+        const int part = ((gi + 1) * p.kw - 1) / NG;
+        uint16_t *at = sx + m * sx_row + part * (p.pos / p.kw) + gi - part * NG / p.kw;
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const __nv_bfloat16 b = __float2bfloat16_rn(s);
+          at[j * MP * sx_row] = __bfloat16_as_ushort(b);
+          s -= __bfloat162float(b);
+        }
+      }
     }
   }
+  __syncthreads();
+
+  // lanes of columns without a vector read the zeros and stay there
+  const uint32_t xb = smem_addr(smem) + (g < MP ? kZero + ((g0 * kWords * MP + g) * 4 + t) * 16 : 0);
+  const uint32_t x_stage = g < MP ? kGps * kWords * MP * 64 : 0;
+  const uint32_t sb = smem_addr(sx) + (g < MP ? (g * sx_row + kp * (p.pos / p.kw) + 2 * t) * 2 : 0);
+  const uint32_t a_lane = ring + g * kRow + t * 4 * kWords;
+  const uint32_t flip = (g % kFlips) * kFlip;
+
+  uint32_t slot = 0;
+  int buf = 0;
+  for (int step = blockIdx.x; step < p.steps; step += gridDim.x, buf ^= 1) {
+    float acc[4] = {}, c_of[4] = {}, c_sc[4] = {};
+    uint32_t xp = xb;
+    for (int st = 0; st < nst; ++st) {
+      const int jb = (st % kSpb) * kGps;
+      if (jb == 0) {
+        const int b = st / kSpb;
 #pragma unroll
-  for (int m = 0; m < M; ++m) {
-    for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
-    if (lane == 0) y[(size_t)m * W.N + row] = acc[m];
+        for (int r = 0; r < 4; ++r) sc[r] = sc_next[r], of[r] = of_next[r];
+        if (st + kSpb < nst) load_scales(step, b + 1);
+        else if (step + (int)gridDim.x < p.steps) load_scales(step + gridDim.x, 0);
+        if (AFFINE) {
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            uint32_t b0 = 0, b1 = 0;
+            if (g < MP) {
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b0) : "r"(sb + (j * MP * sx_row + b * 16) * 2) : "memory");
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b1) : "r"(sb + (j * MP * sx_row + b * 16) * 2 + 16) : "memory");
+            }
+            mma_bf16(c_of, of[0], of[1], of[2], of[3], b0, b1);
+            mma_bf16(c_sc, sc[0], sc[1], sc[2], sc[3], b0, b1);
+          }
+        }
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+      __syncwarp();
+      load_stage();
+      const uint32_t rp = a_lane + slot;
+      slot = slot == (STAGES - 1) * kStage ? 0 : slot + kStage;
+      const int ngs = g1 - g0 - st * kGps;
+      const uint32_t s_row0 = jb & 8 ? sc[2] : sc[0], s_row1 = jb & 8 ? sc[3] : sc[1];
+      uint32_t s_lo = 0, s_hi = 0;  // two groups' scales of rows g and g + 8
+#pragma unroll
+      for (int gi = 0; gi < kGps; ++gi) {
+        if (gi >= ngs) break;
+        if (gi % 2 == 0) {
+          const int from = (lane & ~3) | (((jb >> 1) + (gi >> 1)) & 3);
+          s_lo = __shfl_sync(0xffffffffu, s_row0, from);
+          s_hi = __shfl_sync(0xffffffffu, s_row1, from);
+        }
+        uint32_t a0[kWords], a1[kWords];
+        lds_words<kWords>(a0, rp + (flip ^ (gi * kFlip)));
+        lds_words<kWords>(a1, rp + (flip ^ (gi * kFlip)) + 8 * kRow);
+        float c[4] = {};
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const uint4 b = lds128(xp + (gi * kWords + i) * MP * 64);
+          mma_bf16(c, pair_of<0>(a0[i]), pair_of<0>(a1[i]), pair_of<1>(a0[i]), pair_of<1>(a1[i]), b.x, b.y);
+          mma_bf16(c, pair_of<2>(a0[i]), pair_of<2>(a1[i]), pair_of<3>(a0[i]), pair_of<3>(a1[i]), b.z, b.w);
+        }
+        const float s0 = __uint_as_float(gi & 1 ? s_lo & 0xffff0000u : s_lo << 16);
+        const float s1 = __uint_as_float(gi & 1 ? s_hi & 0xffff0000u : s_hi << 16);
+        acc[0] = fmaf(s0, c[0], acc[0]);
+        acc[1] = fmaf(s0, c[1], acc[1]);
+        acc[2] = fmaf(s1, c[2], acc[2]);
+        acc[3] = fmaf(s1, c[3], acc[3]);
+      }
+      xp += x_stage;
+    }
+    float *rb = red + buf * WARPS * kMaxVec * kTile;
+    float *rw = rb + warp * kMaxVec * kTile + g;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = 2 * t + (r & 1);
+      if (m < MP) rw[m * kTile + 8 * (r >> 1)] = acc[r] + (AFFINE ? fmaf(8.f, c_sc[r], c_of[r]) : 0.f);
+    }
+    __syncthreads();
+    for (int i = tid; i < tps * kMaxVec * kTile; i += WARPS * 32) {
+      const int tile = i / (kMaxVec * kTile), m = i / kTile % kMaxVec;
+      const int row = (step * tps + tile) * kTile + i % kTile;
+      if (m >= M || row >= N) continue;
+      const float *at = rb + tile * (p.kw - 1) * kMaxVec * kTile + i;
+      float s = 0.f;
+      for (int k = 0; k < p.kw; ++k) s += at[k * kMaxVec * kTile];
+      p.y[(size_t)m * N + row] = s;
+    }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 int32_t check_q4(const nslm_q4_matrix *W) {
   if (!W) return NSLM_ERR_ARG;
   if (W->group != 32 && W->group != 64 && W->group != 128) return NSLM_ERR_SHAPE;
-  if (W->N < 0 || W->K <= 0 || W->K % W->group != 0) return NSLM_ERR_SHAPE;
+  if (W->N < 0 || W->N > (1 << 30) || W->K <= 0 || W->K % W->group != 0) return NSLM_ERR_SHAPE;
   if (W->N > 0) {
     if (!W->q || !W->scales) return NSLM_ERR_ARG;
     if (!aligned16(W->q) || !aligned16(W->scales) || !aligned16(W->biases)) return NSLM_ERR_ALIGN;
   }
   return NSLM_OK;
+}
+
+constexpr size_t kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of an SM, and of that for each CTA
+
+// Splits the work for CTAs of `warps` and gives their shared memory.
+size_t q4_plan(Q4Params &p, int mp, int warps, int stages) {
+  // the split of K with the least rounds of work: stages of 256 weights a warp,
+  // and what a tile costs besides (scales, sums, barrier), about one of them
+  const int tiles = ceil_div(p.W.N, kTile), ctas = num_sms() * (warps == 8 ? 2 : 1);
+  int64_t best = INT64_MAX;
+  for (int kw = warps; kw >= 1; kw /= 2) {
+    if (kw > p.NG) continue;
+    const int64_t rounds = ceil_div(ceil_div(tiles, warps / kw), ctas);
+    const int64_t cost = rounds * (ceil_div(ceil_div(p.NG, kw) * p.W.group, kStageK) + 1);
+    if (cost < best) best = cost, p.kw = kw;
+  }
+  p.steps = ceil_div(tiles, warps / p.kw);
+  p.pos = p.kw * 16 * ceil_div(ceil_div(p.NG, p.kw), 16);
+  return kZero + (size_t)2 * mp * p.W.K + (p.W.biases ? (size_t)6 * mp * (p.pos + 8) : 0) +
+         (size_t)warps * stages * kStage + (size_t)2 * warps * kMaxVec * kTile * 4;
+}
+
+template <int G, int MP, int WARPS, int STAGES, bool AFFINE>
+int32_t launch_q4_as(const Q4Params &p, size_t smem, cudaStream_t s) {
+  auto k = q4_gemv_kernel<G, MP, WARPS, STAGES, AFFINE>;
+  if (int32_t st = ensure_smem((const void *)k, smem)) return st;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::min(p.steps, num_sms() * (WARPS == 8 ? 2 : 1)));
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (int32_t st = cuda_status(cudaLaunchKernelEx(&cfg, k, p))) return st;
+  return launch_status();
+}
+
+// Two CTAs of 8 warps on an SM where the activations leave room for both, else
+// one of 16, with a shorter ring for the longest rows.
+template <int G, int MP, bool AFFINE>
+int32_t launch_q4(Q4Params p, cudaStream_t s) {
+  size_t smem = q4_plan(p, MP, 8, 3);
+  if (2 * (smem + kSmemReserved) <= kSmemPerSm) return launch_q4_as<G, MP, 8, 3, AFFINE>(p, smem, s);
+  smem = q4_plan(p, MP, 16, 3);
+  if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 16, 3, AFFINE>(p, smem, s);
+  smem = q4_plan(p, MP, 16, 2);
+  return launch_q4_as<G, MP, 16, 2, AFFINE>(p, smem, s);
+}
+
+template <int G, int MP>
+int32_t launch_q4(const Q4Params &p, cudaStream_t s) {
+  return p.W.biases ? launch_q4<G, MP, true>(p, s) : launch_q4<G, MP, false>(p, s);
+}
+
+template <int G>
+int32_t launch_q4(const Q4Params &p, cudaStream_t s) {
+  return p.M == 1   ? launch_q4<G, 1>(p, s)
+         : p.M == 2 ? launch_q4<G, 2>(p, s)
+         : p.M <= 4 ? launch_q4<G, 4>(p, s)
+                    : launch_q4<G, 8>(p, s);
 }
 
 }  // namespace
@@ -64,15 +392,13 @@ extern "C" int32_t nslm_q4_gemv(const nslm_q4_matrix *W, const uint16_t *x_bf16,
   int32_t st = check_q4(W);
   if (st) return st;
   if (!x_bf16 || !y) return NSLM_ERR_ARG;
-  if (M < 1 || M > kMaxVec || (int64_t)M * W->K > kMaxMK) return NSLM_ERR_SHAPE;
+  if (M < 1 || M > kMaxVec || (int64_t)(M <= 2 ? M : M <= 4 ? 4 : 8) * W->K > kMaxMK) return NSLM_ERR_SHAPE;
   if (!aligned16(x_bf16) || !aligned16(y)) return NSLM_ERR_ALIGN;
   if ((st = check_device())) return st;
   if (W->N == 0) return NSLM_OK;
-  void (*const kernels[])(nslm_q4_matrix, const uint16_t *, float *) = {
-      q4_gemv_kernel<1>, q4_gemv_kernel<2>, q4_gemv_kernel<3>, q4_gemv_kernel<4>,
-      q4_gemv_kernel<5>, q4_gemv_kernel<6>, q4_gemv_kernel<7>, q4_gemv_kernel<8>};
-  kernels[M - 1]<<<(W->N + 7) / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(*W, x_bf16, y);
-  st = launch_status();
+  Q4Params p{*W, x_bf16, y, M, W->K / W->group, 1, 0, 0, (flags & NSLM_GEMV_FIELDS_READY) != 0};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = W->group == 32 ? launch_q4<32>(p, s) : W->group == 64 ? launch_q4<64>(p, s) : launch_q4<128>(p, s);
   if (st == NSLM_OK) g_launches = 1;
   return st;
 }
