@@ -72,6 +72,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
 template <int WORDS>
 __device__ __forceinline__ void lds_words(uint32_t (&a)[WORDS], uint32_t at) {
   if constexpr (WORDS == 1) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a[0]) : "r"(at) : "memory");
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
   constexpr int kFlip = G / 2;         // in units of a group's bytes
   constexpr int kFlips = kRow / kFlip; // 8, 4 or 2
   extern __shared__ uint4 smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int M = p.M, K = p.W.K, N = p.W.N, NG = p.NG;
   uint4 *xs = smem + kZero / 16;  // [K / 32][MP][4], behind the zeros
   uint16_t *sx = reinterpret_cast<uint16_t *>(xs + (size_t)MP * K / 8);  // [3][MP][pos + 8]
@@ -145,35 +150,43 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // scales and offsets of 16 groups in the A fragment's layout, one batch ahead
+  // scales and offsets of 16 groups, one batch ahead: lane t has groups 4t..4t+3
+  // of rows g (words 0, 1) and g + 8 (2, 3), which is the A fragment of a
+  // product over the groups in that order
   uint32_t sc[4], of[4], sc_next[4], of_next[4];
-  const bool paired = ((NG | g0 | (g1 - g0)) & 1) == 0;  // two groups' values lie in one aligned word
-  auto load_scales = [&](int step, int b) {
-    const int row = (step * tps + sub) * kTile + g;
+  int c_step = blockIdx.x, c_b = 0;
+  const bool quads = ((NG | g0) & 3) == 0;  // four groups' values lie in one aligned word of 8 bytes
+  auto load_scales = [&]() {
+    if (c_step >= p.steps) return;
+    const int row = (c_step * tps + sub) * kTile + g, gi = g0 + c_b * 16 + 4 * t;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int gi = g0 + b * 16 + 2 * t + 8 * (r >> 1);
-      const size_t at = (size_t)min(row + 8 * (r & 1), N - 1) * NG + gi;
-      sc_next[r] = of_next[r] = 0;
-      if (gi - 2 * t >= g1) continue;
-      if (paired) {
-        if (gi < g1) {
-          sc_next[r] = __ldg(reinterpret_cast<const uint32_t *>(p.W.scales + at));
-          if (AFFINE) of_next[r] = __ldg(reinterpret_cast<const uint32_t *>(p.W.biases + at));
+    for (int r = 0; r < 2; ++r) {
+      const size_t at = (size_t)min(row + 8 * r, N - 1) * NG + gi;
+      uint2 s = make_uint2(0, 0), o = make_uint2(0, 0);
+      if (quads) {
+        if (gi < NG) {  // past the range's end the next warp's, where the sums of x are zero
+          s = __ldg(reinterpret_cast<const uint2 *>(p.W.scales + at));
+          if (AFFINE) o = __ldg(reinterpret_cast<const uint2 *>(p.W.biases + at));
         }
       } else {
+        uint32_t v[4] = {}, w[4] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 4; ++h)
           if (gi + h < g1) {
-            sc_next[r] |= (uint32_t)__ldg(p.W.scales + at + h) << (16 * h);
-            if (AFFINE) of_next[r] |= (uint32_t)__ldg(p.W.biases + at + h) << (16 * h);
+            v[h] = __ldg(p.W.scales + at + h);
+            if (AFFINE) w[h] = __ldg(p.W.biases + at + h);
           }
+        s = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+        o = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
       }
+      sc_next[2 * r] = s.x, sc_next[2 * r + 1] = s.y;
+      of_next[2 * r] = o.x, of_next[2 * r + 1] = o.y;
     }
+    if (++c_b * 16 >= g1 - g0) c_b = 0, c_step += gridDim.x;
   };
   auto prologue = [&]() {
     for (int i = 0; i < STAGES - 1; ++i) load_stage();
-    if (blockIdx.x < p.steps) load_scales(blockIdx.x, 0);
+    load_scales();
   };
 
   if (p.ready) prologue();
@@ -187,9 +200,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
   if (!p.ready) prologue();
 
   // activations: word wi of a group is what lane wi / kWords multiplies in step wi % kWords
-  for (int i = tid; i < MP * K / 8; i += WARPS * 32) {
-    const int m = i / (K / 8), w = i - m * (K / 8), gi = w / (G / 8), wi = w - gi * (G / 8);
-    const uint4 v = m < M ? __ldg(reinterpret_cast<const uint4 *>(p.x) + i) : make_uint4(0, 0, 0, 0);
+  for (int m = 0; m < MP; ++m)
+  for (int w = tid; w < K / 8; w += WARPS * 32) {
+    const int gi = w / (G / 8), wi = w % (G / 8);
+    const uint4 v = m < M ? __ldg(reinterpret_cast<const uint4 *>(p.x) + (size_t)m * (K / 8) + w) : make_uint4(0, 0, 0, 0);
     const uint4 q = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
     xs[((size_t)(gi * kWords + wi % kWords) * MP + m) * 4 + wi / kWords] = q;
@@ -199,7 +213,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
 #pragma unroll
       for (int j = 0; j < 4; ++j) s += bf16_f32(h[j] & 0xffffu) + __uint_as_float(h[j] & 0xffff0000u);
       // G / 8 neighbouring lanes hold a group; groups do not straddle the end
-      const int left = MP * K / 8 - (i - lane);
+      const int left = K / 8 - (w - lane);
       const uint32_t mask = left >= 32 ? 0xffffffffu : (1u << left) - 1;
 #pragma unroll
       for (int o = 1; o < G / 8; o <<= 1) s += __shfl_xor_sync(mask, s, o);
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
   // lanes of columns without a vector read the zeros and stay there
   const uint32_t xb = smem_addr(smem) + (g < MP ? kZero + ((g0 * kWords * MP + g) * 4 + t) * 16 : 0);
   const uint32_t x_stage = g < MP ? kGps * kWords * MP * 64 : 0;
-  const uint32_t sb = smem_addr(sx) + (g < MP ? (g * sx_row + kp * (p.pos / p.kw) + 2 * t) * 2 : 0);
+  const uint32_t sb = smem_addr(sx) + (g < MP ? (g * sx_row + kp * (p.pos / p.kw) + 4 * t) * 2 : 0);
   const uint32_t a_lane = ring + g * kRow + t * 4 * kWords;
   const uint32_t flip = (g % kFlips) * kFlip;
 
@@ -230,23 +244,18 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
     float acc[4] = {}, c_of[4] = {}, c_sc[4] = {};
     uint32_t xp = xb;
     for (int st = 0; st < nst; ++st) {
-      const int jb = (st % kSpb) * kGps;
+      const int jb = (st % kSpb) * kGps;  // the stage's first group in its batch
       if (jb == 0) {
-        const int b = st / kSpb;
 #pragma unroll
         for (int r = 0; r < 4; ++r) sc[r] = sc_next[r], of[r] = of_next[r];
-        if (st + kSpb < nst) load_scales(step, b + 1);
-        else if (step + (int)gridDim.x < p.steps) load_scales(step + gridDim.x, 0);
+        load_scales();
         if (AFFINE) {
 #pragma unroll
           for (int j = 0; j < 3; ++j) {
-            uint32_t b0 = 0, b1 = 0;
-            if (g < MP) {
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b0) : "r"(sb + (j * MP * sx_row + b * 16) * 2) : "memory");
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b1) : "r"(sb + (j * MP * sx_row + b * 16) * 2 + 16) : "memory");
-            }
-            mma_bf16(c_of, of[0], of[1], of[2], of[3], b0, b1);
-            mma_bf16(c_sc, sc[0], sc[1], sc[2], sc[3], b0, b1);
+            uint2 b = make_uint2(0, 0);
+            if (g < MP) b = lds64(sb + (j * MP * sx_row + st / kSpb * 16) * 2);
+            mma_bf16(c_of, of[0], of[2], of[1], of[3], b.x, b.y);
+            mma_bf16(c_sc, sc[0], sc[2], sc[1], sc[3], b.x, b.y);
           }
         }
       }
@@ -255,16 +264,12 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
       load_stage();
       const uint32_t rp = a_lane + slot;
       slot = slot == (STAGES - 1) * kStage ? 0 : slot + kStage;
-      const int ngs = g1 - g0 - st * kGps;
-      const uint32_t s_row0 = jb & 8 ? sc[2] : sc[0], s_row1 = jb & 8 ? sc[3] : sc[1];
       uint32_t s_lo = 0, s_hi = 0;  // two groups' scales of rows g and g + 8
-#pragma unroll
-      for (int gi = 0; gi < kGps; ++gi) {
-        if (gi >= ngs) break;
+      auto group = [&](int gi) {
         if (gi % 2 == 0) {
-          const int from = (lane & ~3) | (((jb >> 1) + (gi >> 1)) & 3);
-          s_lo = __shfl_sync(0xffffffffu, s_row0, from);
-          s_hi = __shfl_sync(0xffffffffu, s_row1, from);
+          const int from = (lane & ~3) | ((jb | gi) >> 2), word = ((jb | gi) >> 1) & 1;
+          s_lo = __shfl_sync(0xffffffffu, word ? sc[1] : sc[0], from);
+          s_hi = __shfl_sync(0xffffffffu, word ? sc[3] : sc[2], from);
         }
         uint32_t a0[kWords], a1[kWords];
         lds_words<kWords>(a0, rp + (flip ^ (gi * kFlip)));
@@ -282,6 +287,15 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
         acc[1] = fmaf(s0, c[1], acc[1]);
         acc[2] = fmaf(s1, c[2], acc[2]);
         acc[3] = fmaf(s1, c[3], acc[3]);
+      };
+      const int ngs = g1 - g0 - st * kGps;
+      if (ngs >= kGps) {
+#pragma unroll
+        for (int gi = 0; gi < kGps; ++gi) group(gi);
+      } else {  // the end of the range
+#pragma unroll
+        for (int gi = 0; gi < kGps - 1; ++gi)
+          if (gi < ngs) group(gi);
       }
       xp += x_stage;
     }
@@ -359,10 +373,12 @@ int32_t launch_q4_as(const Q4Params &p, size_t smem, cudaStream_t s) {
 // one of 16, with a shorter ring for the longest rows.
 template <int G, int MP, bool AFFINE>
 int32_t launch_q4(Q4Params p, cudaStream_t s) {
-  size_t smem = q4_plan(p, MP, 8, 3);
+  size_t smem = q4_plan(p, MP, 8, 5);
+  if (2 * (smem + kSmemReserved) <= kSmemPerSm) return launch_q4_as<G, MP, 8, 5, AFFINE>(p, smem, s);
+  smem = q4_plan(p, MP, 8, 3);
   if (2 * (smem + kSmemReserved) <= kSmemPerSm) return launch_q4_as<G, MP, 8, 3, AFFINE>(p, smem, s);
-  smem = q4_plan(p, MP, 16, 3);
-  if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 16, 3, AFFINE>(p, smem, s);
+  smem = q4_plan(p, MP, 16, 4);
+  if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 16, 4, AFFINE>(p, smem, s);
   smem = q4_plan(p, MP, 16, 2);
   return launch_q4_as<G, MP, 16, 2, AFFINE>(p, smem, s);
 }
