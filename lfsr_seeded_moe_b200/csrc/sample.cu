@@ -1,6 +1,7 @@
 // sample.cu -- nslm_sample: one token a row from logits, with temperature,
 // top-k, top-p and min-p, at given random numbers.
 #include <algorithm>
+#include <cfloat>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -13,11 +14,11 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxV = 1 << 18;
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 512;
 constexpr int kList = 256;
-constexpr int kLevels = 4;
+constexpr int kLevels = 6;  // and all as the last
 
 struct SampleParams {
   const void *logits;
@@ -45,15 +46,13 @@ struct SampleParams {
 // never wait for one another.
 struct Weight {
   float m;       // the row's largest logit
-  bool greedy;   // only the logits equal to m have a weight, and it is 1
+  float low;     // 40 temperatures below, where weights have long been 0: what is lower is not looked at
   double step;   // 16 / (temperature ln 2)
   const double *pow16;  // shared: 2^(44 + j/16)
 
   __device__ __forceinline__ double operator()(float v) const {
-    if (greedy) return v == m ? 0x1p44 : 0.;
     const double t = ((double)v - (double)m) * step;
-    if (!(t >= -16. * 46.)) return 0.;  // below 2^-45, and what is not to be drawn (v = -inf)
-    const double kd = t + 0x1.8p52;     // t to the nearest integer, in the low bits
+    const double kd = t + 0x1.8p52;  // t to the nearest integer, in the low bits
     const int k = __double2loint(kd);
     const double r = t - (kd - 0x1.8p52);
     // (ln 2 / 16)^i / i!
@@ -64,20 +63,13 @@ struct Weight {
     e = fma(e, r, 0x1.62e42fefa39efp-5);
     e = fma(e, r, 1.);
     const double w = e * pow16[k & 15];
-    return __hiloint2double(__double2hiint(w) + ((k >> 4) << 20), __double2loint(w));
+    return v >= low ? __hiloint2double(__double2hiint(w) + ((k >> 4) << 20), __double2loint(w)) : 0.;
   }
   __device__ __forceinline__ uint64_t fixed(float v) const { return to_fixed((*this)(v)); }
   // to the nearest integer: below 2^51 it stands in the low bits of w + 2^52
   static __device__ __forceinline__ uint64_t to_fixed(double w) {
     return (uint64_t)__double_as_longlong(w + 0x1p52) & 0xfffffffffffffull;
   }
-};
-
-// What the CTAs of a row tell one another.
-struct Part {
-  uint64_t mass[kLevels + 1];
-  uint32_t count[kLevels + 1];
-  float lo, hi;
 };
 
 struct Candidate {
@@ -88,13 +80,14 @@ struct Candidate {
 
 struct Shared {
   double pow16[16];
-  Part part[2][kMaxCluster];
-  uint64_t warp_mass[kWarps][kLevels + 1];
-  uint32_t warp_count[kWarps][kLevels + 1];
-  float warp_lo[kWarps], warp_hi[kWarps];
+  // what every warp of the row tells every CTA, by turns
+  uint64_t slot[2][kLevels + 1][kMaxCluster * kWarps];
+  uint64_t warp_mass[kWarps];
+  uint32_t warp_count[kWarps];
   int32_t list_n;
   int32_t found;
-  uint64_t found_before;
+  uint64_t found_mass;
+  uint32_t found_count, found_in;
   union {
     struct {
       uint32_t count[kBins], lo[kBins], hi[kBins];
@@ -106,6 +99,14 @@ struct Shared {
 template <class T> __device__ __forceinline__ T warp_sum_of(T v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <class T> __device__ __forceinline__ T warp_scan_of(T v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
   return v;
 }
 
@@ -125,15 +126,22 @@ struct Range {
   __device__ __forceinline__ bool has(float v) const { return v >= lo && v < top && (bin < 0 || bin_of(v) == bin); }
 };
 
+// Counts, and masses, of the tokens with logits from m down to some levels below, and of all.
+struct Levels {
+  uint64_t mass[kLevels + 1];
+  uint32_t count[kLevels + 1];
+};
+
 struct Row {
-  const SampleParams &p;
   Shared &s;
-  const float *l;   // shared: this CTA's logits
-  int n;            // how many
-  int first;        // the index of the first
-  int rank, ctas;   // in the cluster
+  const float *l;  // shared: this CTA's logits
+  int n;           // how many
+  int first;       // the index of the first
+  int rank, ctas;  // in the cluster
+  int warp, lane;
   int parity = 0;
-  Weight w;
+  float temp = 1.f, lowest = 0.f;
+  Weight w{};
   // the last token that stays, in the order of descending logits and ascending indexes
   float last_v = -INFINITY;
   int last_i = kMaxV;
@@ -145,20 +153,16 @@ struct Row {
   // A warp's share of the CTA's logits: contiguous, so that sums over warps are sums over indexes.
   __device__ __forceinline__ int share() const { return ((n + kWarps - 1) / kWarps + 31) & ~31; }
 
-  // Every CTA's part in every CTA; `mine` is taken from thread 0.
-  __device__ const Part *exchange(const Part &mine) {
-    Part *slots = s.part[parity];
-    parity ^= 1;
-    if (ctas == 1) {
-      if (threadIdx.x == 0) slots[0] = mine;
-      __syncthreads();
-      return slots;
+  // f(i, logit) for this thread's logits, four at a time so that their
+  // latencies overlap; i of a place past the end is meaningless, its logit -inf.
+  template <class F> __device__ __forceinline__ void each(F f) const {
+    for (int i = threadIdx.x; i < n; i += 4 * kThreads) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = i + j * kThreads < n ? l[i + j * kThreads] : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f(i + j * kThreads, v[j]);
     }
-    cg::cluster_group cluster = cg::this_cluster();
-    if (threadIdx.x == 0)
-      for (int r = 0; r < ctas; ++r) *cluster.map_shared_rank(&slots[rank], r) = mine;
-    cluster.sync();
-    return slots;
   }
 
   __device__ void sync_row() {
@@ -166,112 +170,215 @@ struct Row {
     else cg::this_cluster().sync();
   }
 
-  // Sums of `parts` masses and counts over the row.
-  __device__ Part sum_row(uint64_t (&mass)[kLevels + 1], uint32_t (&count)[kLevels + 1], int parts) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int j = 0; j < parts; ++j) {
-      const uint64_t a = warp_sum_of(mass[j]);
-      const uint32_t c = warp_sum_of(count[j]);
-      if (lane == 0) s.warp_mass[warp][j] = a, s.warp_count[warp][j] = c;
+  // Every warp's values (the same in all its lanes) to every CTA.  Two sets of
+  // slots by turns: who writes one again has passed the barrier after which
+  // the others had read it.
+  using Slots = const uint64_t (*)[kMaxCluster * kWarps];
+  template <int V> __device__ __forceinline__ Slots publish(const uint64_t (&v)[V]) {
+    auto slot = s.slot[parity];
+    parity ^= 1;
+    if (lane < ctas) {
+      uint64_t *to = ctas == 1 ? &slot[0][0] : cg::this_cluster().map_shared_rank(&slot[0][0], lane);
+#pragma unroll
+      for (int j = 0; j < V; ++j) to[j * kMaxCluster * kWarps + rank * kWarps + warp] = v[j];
     }
-    __syncthreads();
-    Part t{};
-    if (threadIdx.x == 0)
-      for (int k = 0; k < kWarps; ++k)
-        for (int j = 0; j < parts; ++j) t.mass[j] += s.warp_mass[k][j], t.count[j] += s.warp_count[k][j];
-    const Part *all = exchange(t);
-    t = Part{};
-    for (int r = 0; r < ctas; ++r)
-      for (int j = 0; j < parts; ++j) t.mass[j] += all[r].mass[j], t.count[j] += all[r].count[j];
-    return t;
+    sync_row();
+    return slot;
+  }
+
+  // Smallest and largest over the row.
+  __device__ void extremes(float &lo, float &hi) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    const uint64_t v[1] = {(uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo)};
+    const auto slot = publish(v);
+    for (int k = lane; k < ctas * kWarps; k += 32) {
+      lo = fminf(lo, __uint_as_float((uint32_t)slot[0][k]));
+      hi = fmaxf(hi, __uint_as_float((uint32_t)(slot[0][k] >> 32)));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
   }
 
   // The lowest index for which the sum of f up to it exceeds target(the whole
-  // sum), as the position in the CTA that has it, -1 in the others; before:
-  // the sum below that index; all: the whole sum.
-  template <class F, class G>
-  __device__ int find(F f, G target, uint64_t &all) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // sum all), as the position in the CTA that has it, valid in one warp of
+  // that CTA; -1 everywhere else.
+  template <class F, class G> __device__ int find(F f, G target, uint64_t &all) {
     const int per = share();
     auto sum = [&](int lo, int hi) {
       uint64_t a = 0;
-      for (int i = lo + lane; i < hi; i += 32) a += f(i, l[i]);
+      for (int i = lo + lane; i < hi; i += 128) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a += f(i + 32 * j, i + 32 * j < hi ? l[i + 32 * j] : -INFINITY);
+      }
       return warp_sum_of(a);
     };
-    __syncthreads();
-    const uint64_t a = sum(warp * per, min(n, (warp + 1) * per));
-    if (lane == 0) s.warp_mass[warp][0] = a;
-    __syncthreads();
-    Part mine{};
-    if (threadIdx.x == 0)
-      for (int k = 0; k < kWarps; ++k) mine.mass[0] += s.warp_mass[k][0];
-    const Part *parts = exchange(mine);
-    uint64_t before = 0, own = parts[rank].mass[0];
+    const uint64_t v[1] = {sum(warp * per, min(n, (warp + 1) * per))};
+    const auto slot = publish(v);
+    // the warp of the row that has it
+    uint64_t x[kMaxCluster * kWarps / 32];
     all = 0;
-    for (int r = 0; r < ctas; ++r) {
-      if (r < rank) before += parts[r].mass[0];
-      all += parts[r].mass[0];
-    }
-    const uint64_t t = target(all);
-    if (t < before || t - before >= own) return -1;
-    // the warp that has it, then the same over that warp's logits
-    uint64_t left = t - before;
-    int at = 0;
-    while (at < kWarps - 1 && left >= s.warp_mass[at][0]) left -= s.warp_mass[at++][0];
-    __syncthreads();
-    const int lo = at * per, hi = min(n, lo + per), sub = (per / kWarps + 31) & ~31;
-    const uint64_t c = sum(lo + warp * sub, min(hi, lo + (warp + 1) * sub));
-    if (lane == 0) s.warp_mass[warp][0] = c;
-    __syncthreads();
-    at = 0;
-    while (at < kWarps - 1 && left >= s.warp_mass[at][0]) left -= s.warp_mass[at++][0];
-    if (warp == 0) {
-      for (int i = lo + at * sub + lane; i - lane < hi; i += 32) {
-        uint64_t x = i < hi ? f(i, l[i]) : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        const uint32_t over = __ballot_sync(0xffffffffu, x > left);
-        if (over) {
-          if (lane == 0) s.found = i + __ffs(over) - 1;
-          break;
-        }
-        left -= __shfl_sync(0xffffffffu, x, 31);
+    for (int j = 0; j < kMaxCluster * kWarps / 32; ++j) {
+      x[j] = 32 * j + lane < ctas * kWarps ? slot[0][32 * j + lane] : 0;
+      all += x[j];
+    }
+    all = warp_sum_of(all);
+    uint64_t left = target(all);
+    int at = -1;
+#pragma unroll
+    for (int j = 0; j < kMaxCluster * kWarps / 32; ++j) {
+      const uint64_t upto = warp_scan_of(x[j], lane);
+      const uint32_t over = __ballot_sync(0xffffffffu, upto > left);
+      if (at >= 0) continue;
+      if (over) {
+        const int k = __ffs(over) - 1;
+        at = 32 * j + k;
+        left -= __shfl_sync(0xffffffffu, upto - x[j], k);
+      } else {
+        left -= __shfl_sync(0xffffffffu, upto, 31);
       }
     }
-    __syncthreads();
-    return s.found;
+    if (at < 0 || at / kWarps != rank) return -1;
+    at %= kWarps;
+    int lo = at * per, hi = min(n, lo + per);
+    if (per > 256) {  // all warps on that warp's logits
+      const int sub = (per / kWarps + 31) & ~31;
+      const uint64_t c = sum(lo + warp * sub, min(hi, lo + (warp + 1) * sub));
+      if (lane == 0) s.warp_mass[warp] = c;
+      __syncthreads();
+      at = 0;
+      while (at < kWarps - 1 && left >= s.warp_mass[at]) left -= s.warp_mass[at++];
+      lo += at * sub;
+      hi = min(hi, lo + sub);
+    }
+    if (warp != at) return -1;
+    for (int i = lo; i < hi; i += 32) {
+      const uint64_t upto = warp_scan_of(f(i + lane, i + lane < hi ? l[i + lane] : -INFINITY), lane);
+      const uint32_t over = __ballot_sync(0xffffffffu, upto > left);
+      if (over) return i + __ffs(over) - 1;
+      left -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return -1;
   }
 
+  // The levels, in temperatures below m.
+  __device__ __forceinline__ float level(int j) const {
+    constexpr float below[kLevels] = {2.f, 4.f, 6.f, 8.f, 11.f, 15.f};
+    float c = below[0];
+#pragma unroll
+    for (int i = 1; i < kLevels; ++i) c = j == i ? below[i] : c;
+    return __fmaf_rn(-temp, c, w.m);
+  }
+  template <bool MASS> __device__ Levels levels() {
+    float at[kLevels];
+#pragma unroll
+    for (int j = 0; j < kLevels; ++j) at[j] = level(j);
+    // a thread has at most 64 logits: its counts stand in bytes, or above bit 51 of its mass, which needs 51
+    uint64_t sum[kLevels + 1] = {};
+    uint32_t bytes[2] = {};
+    each([&](int i, float v) {
+      if (!(v > -INFINITY && kept(i, v))) return;
+      if (MASS) {
+        const uint64_t x = w.fixed(v) | 1ull << 52;
+        sum[kLevels] += x;
+#pragma unroll
+        for (int j = 0; j < kLevels; ++j)
+          if (v >= at[j]) sum[j] += x;
+      } else {
+        bytes[kLevels / 4] += 1u << (8 * (kLevels % 4));
+#pragma unroll
+        for (int j = 0; j < kLevels; ++j)
+          if (v >= at[j]) bytes[j / 4] += 1u << (8 * (j % 4));
+      }
+    });
+    Levels t{};
+    auto add = [&](Slots slot, auto put) {
+#pragma unroll
+      for (int j = 0; j <= kLevels; ++j) {
+        uint64_t a = 0;
+        for (int k = lane; k < ctas * kWarps; k += 32) a += slot[j][k];
+        put(j, warp_sum_of(a));
+      }
+    };
+    if (MASS) {
+      uint64_t v[kLevels + 1];
+#pragma unroll
+      for (int j = 0; j <= kLevels; ++j) {
+        v[j] = warp_sum_of(sum[j] & 0xfffffffffffffull);
+        sum[j] = warp_sum_of((uint32_t)(sum[j] >> 52));
+      }
+      add(publish(v), [&](int j, uint64_t a) { t.mass[j] = a; });
+    } else {
+#pragma unroll
+      for (int j = 0; j <= kLevels; ++j) sum[j] = warp_sum_of(bytes[j / 4] >> (8 * (j % 4)) & 255u);
+    }
+    add(publish(sum), [&](int j, uint64_t a) { t.count[j] = (uint32_t)a; });
+    return t;
+  }
+  // The tokens of level j that are not of the one before.
+  __device__ Range range_of(int j, const Levels &t) const {
+    Range r;
+    r.lo = j < kLevels ? fmaxf(level(j), lowest) : lowest;
+    r.top = j > 0 ? level(j - 1) : INFINITY;
+    r.hi = fminf(r.top, w.m);
+    r.above_mass = j > 0 ? t.mass[j - 1] : 0;
+    r.above_count = j > 0 ? t.count[j - 1] : 0;
+    return r;
+  }
+
+  // The kept tokens of a range, at most kList, in CTA 0's list.
+  __device__ void gather(const Range &r) {
+    if (threadIdx.x == 0) s.list_n = 0;
+    sync_row();
+    Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, 0);
+    each([&](int i, float v) {
+      if (r.has(v) && kept(i, v)) o->list[atomicAdd(&o->list_n, 1)] = Candidate{w.fixed(v), v, first + i};
+    });
+    sync_row();
+  }
+  // The sum of f over the list, in each of `per` threads.
+  template <class F> __device__ __forceinline__ uint64_t over_list(int n, int per, F f) {
+    uint64_t a = 0;
+#pragma unroll 4
+    for (int j = threadIdx.x & (per - 1); j < n; j += per) a += f(s.list[j]);
+    for (int o = 1; o < per; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+  }
+  // threads for each of n candidates
+  __device__ __forceinline__ static int threads_each(int n) { return n <= 64 ? 8 : n <= 128 ? 4 : 2; }
+
   // Sets the last token that stays to the one at which the kept tokens' count
-  // (by_mass: their mass), in their order, first reaches `need`; all of them
-  // together reach it.
+  // (by_mass: their mass), in their order, first reaches `need`, which is in
+  // the range of `in` tokens.
   __device__ void cut(uint64_t need, bool by_mass, Range r, uint32_t in) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto inside = [&](int i) { return kept(i, l[i]) && r.has(l[i]); };
+    auto inside = [&](int i, float v) { return r.has(v) && kept(i, v); };
     while (in > kList && r.lo < r.hi) {
       // a histogram of the range; the bin that has the token is the next range
+      __syncthreads();
       for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist.count[b] = s.hist.lo[b] = s.hist.hi[b] = 0;
       __syncthreads();
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        if (!inside(i)) continue;
-        const int b = r.bin_of(l[i]);
+      each([&](int i, float v) {
+        if (!inside(i, v)) return;
+        const int b = r.bin_of(v);
         atomicAdd(&s.hist.count[b], 1u);
         if (by_mass) {
-          const uint64_t x = w.fixed(l[i]);
+          const uint64_t x = w.fixed(v);
           const uint32_t lo = (uint32_t)x, old = atomicAdd(&s.hist.lo[b], lo);
           atomicAdd(&s.hist.hi[b], (uint32_t)(x >> 32) + (old + lo < lo ? 1u : 0u));
         }
-      }
+      });
       sync_row();
       // every CTA adds all histograms and finds the bin
       constexpr int kPer = kBins / kThreads;
-      uint64_t mass[kPer];
-      uint32_t count[kPer];
-      uint64_t m = 0;
-      uint32_t c = 0;
+      uint64_t mass[kPer], m = 0;
+      uint32_t count[kPer], c = 0;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
         const int b = threadIdx.x * kPer + q;
@@ -283,72 +390,51 @@ struct Row {
         }
         m += mass[q], c += count[q];
       }
-      // running sums over the threads
-      uint64_t ms = m;
-      uint32_t cs = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, ms, o);
-        const uint32_t z = __shfl_up_sync(0xffffffffu, cs, o);
-        if (lane >= o) ms += y, cs += z;
-      }
-      if (lane == 31) s.warp_mass[warp][0] = ms, s.warp_count[warp][0] = cs;
+      uint64_t ms = warp_scan_of(m, lane);
+      uint32_t cs = warp_scan_of(c, lane);
+      if (lane == 31) s.warp_mass[warp] = ms, s.warp_count[warp] = cs;
       __syncthreads();
       ms += r.above_mass - m, cs += r.above_count - c;
-      for (int k = 0; k < warp; ++k) ms += s.warp_mass[k][0], cs += s.warp_count[k][0];
+      for (int k = 0; k < warp; ++k) ms += s.warp_mass[k], cs += s.warp_count[k];
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
         const uint64_t from = by_mass ? ms : cs, to = from + (by_mass ? mass[q] : count[q]);
-        if (from < need && need <= to) {
-          s.found = threadIdx.x * kPer + q;
-          s.found_before = ms;
-          s.list_n = (int32_t)cs;
-          s.warp_count[0][1] = count[q];
-        }
+        if (from < need && need <= to)
+          s.found = threadIdx.x * kPer + q, s.found_mass = ms, s.found_count = cs, s.found_in = count[q];
         ms += mass[q], cs += count[q];
       }
       __syncthreads();
       r.bin = s.found;
-      r.above_mass = s.found_before;
-      r.above_count = (uint32_t)s.list_n;
-      in = s.warp_count[0][1];
+      r.above_mass = s.found_mass;
+      r.above_count = s.found_count;
+      in = s.found_in;
       if (in <= kList) break;
       // its logits' smallest and largest
       float lo = INFINITY, hi = -INFINITY;
-      for (int i = threadIdx.x; i < n; i += kThreads)
-        if (inside(i)) lo = fminf(lo, l[i]), hi = fmaxf(hi, l[i]);
+      each([&](int i, float v) {
+        if (inside(i, v)) lo = fminf(lo, v), hi = fmaxf(hi, v);
+      });
       extremes(lo, hi);
       r.lo = lo, r.hi = hi, r.bin = -1;
       r.top = nextafterf(hi, INFINITY);
     }
-    Part found{};
+    uint64_t found[1] = {0};  // the token's index and logit
     if (in <= kList) {
-      // few enough: CTA 0 orders them
-      __syncthreads();
-      if (threadIdx.x == 0) s.list_n = 0;
-      sync_row();
-      Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, 0);
-      for (int i = threadIdx.x; i < n; i += kThreads)
-        if (inside(i)) o->list[atomicAdd(&o->list_n, 1)] = Candidate{w.fixed(l[i]), l[i], first + i};
-      sync_row();
-      if (rank == 0) {
-        const int c = threadIdx.x;
-        if (c < s.list_n) {
-          const Candidate x = s.list[c];
-          uint64_t before = by_mass ? r.above_mass : r.above_count;
-          for (int j = 0; j < s.list_n; ++j) {
-            const Candidate y = s.list[j];
-            if (y.v > x.v || (y.v == x.v && y.i < x.i)) before += by_mass ? y.w : 1;
-          }
-          if (before < need && need <= before + (by_mass ? x.w : 1)) s.warp_lo[0] = x.v, s.found = x.i;
-        }
+      gather(r);
+      if (rank == 0) {  // few enough: CTA 0 orders them
+        const int len = s.list_n, per = threads_each(len), c = threadIdx.x / per;
+        const Candidate x = s.list[min(c, len - 1)];
+        const uint64_t before = (by_mass ? r.above_mass : r.above_count) + over_list(len, per, [&](const Candidate &y) {
+          return y.v > x.v || (y.v == x.v && y.i < x.i) ? (by_mass ? y.w : 1) : 0;
+        });
+        if (c < len && before < need && need <= before + (by_mass ? x.w : 1))
+          s.found_mass = (uint64_t)__float_as_uint(x.v) << 32 | (uint32_t)x.i;
         __syncthreads();
-        found.lo = s.warp_lo[0];
-        found.count[0] = s.found;
+        found[0] = s.found_mass;
       }
-      const Part *all = exchange(found);
-      last_v = all[0].lo;
-      last_i = (int)all[0].count[0];
+      const uint64_t x = publish(found)[0][0];
+      last_v = __uint_as_float((uint32_t)(x >> 32));
+      last_i = (int)(uint32_t)x;
     } else {
       // equal logits: by their indexes
       const float v = r.lo;
@@ -360,65 +446,13 @@ struct Row {
       uint64_t all;
       const int at = find([&](int i, float y) -> uint64_t { return y == v && kept(i, y); },
                           [&](uint64_t) { return rest - 1; }, all);
-      found.count[0] = at >= 0 ? first + at + 1 : 0;
-      const Part *parts = exchange(found);
+      found[0] = at >= 0 ? first + at + 1 : 0;  // in one warp of the row
+      const auto slot = publish(found);
+      uint64_t a = 0;
+      for (int k = lane; k < ctas * kWarps; k += 32) a += slot[0][k];
       last_v = v;
-      for (int k = 0; k < ctas; ++k)
-        if (parts[k].count[0]) last_i = (int)parts[k].count[0] - 1;
+      last_i = (int)warp_sum_of(a) - 1;
     }
-  }
-
-  // Smallest and largest over the row.
-  __device__ void extremes(float &lo, float &hi) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    if (lane == 0) s.warp_lo[warp] = lo, s.warp_hi[warp] = hi;
-    __syncthreads();
-    Part t{};
-    t.lo = INFINITY, t.hi = -INFINITY;
-    if (threadIdx.x == 0)
-      for (int k = 0; k < kWarps; ++k) t.lo = fminf(t.lo, s.warp_lo[k]), t.hi = fmaxf(t.hi, s.warp_hi[k]);
-    const Part *all = exchange(t);
-    lo = INFINITY, hi = -INFINITY;
-    for (int r = 0; r < ctas; ++r) lo = fminf(lo, all[r].lo), hi = fmaxf(hi, all[r].hi);
-  }
-
-  // The tokens with logits from m down to 3, 7, 12 and 20 temperatures below,
-  // and all: how many they are, and their mass.
-  __device__ __forceinline__ float level(int j, float temp) const {
-    return __fmaf_rn(-temp, j == 0 ? 3.f : j == 1 ? 7.f : j == 2 ? 12.f : 20.f, w.m);
-  }
-  __device__ Part levels(float temp, bool by_mass) {
-    uint64_t mass[kLevels + 1] = {};
-    uint32_t count[kLevels + 1] = {};
-    float at[kLevels];
-#pragma unroll
-    for (int j = 0; j < kLevels; ++j) at[j] = level(j, temp);
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float v = l[i];
-      if (v == -INFINITY || !kept(i, v)) continue;
-      const uint64_t x = by_mass ? w.fixed(v) : 0;
-      mass[kLevels] += x, ++count[kLevels];
-#pragma unroll
-      for (int j = 0; j < kLevels; ++j)
-        if (v >= at[j]) mass[j] += x, ++count[j];
-    }
-    return sum_row(mass, count, kLevels + 1);
-  }
-  __device__ void cut_level(uint64_t need, bool by_mass, float temp, float lowest, const Part &t) {
-    int j = 0;
-    while (j < kLevels && (by_mass ? t.mass[j] : t.count[j]) < need) ++j;
-    Range r;
-    r.lo = j < kLevels ? fmaxf(level(j, temp), lowest) : lowest;
-    r.top = j > 0 ? level(j - 1, temp) : INFINITY;
-    r.hi = fminf(r.top, w.m);
-    r.above_mass = j > 0 ? t.mass[j - 1] : 0;
-    r.above_count = j > 0 ? t.count[j - 1] : 0;
-    cut(need, by_mass, r, t.count[j] - r.above_count);
   }
 };
 
@@ -427,7 +461,7 @@ __device__ __forceinline__ float logit_of(float v) { return v == v ? v : -INFINI
 __device__ __forceinline__ float logit_of(__nv_bfloat16 v) { return logit_of(__bfloat162float(v)); }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ float4 s_logits[];
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
@@ -450,6 +484,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     return v;
   };
   const int vecs = (n - head) / kVec;
+#pragma unroll 4
   for (int i = tid; i < vecs; i += kThreads) {
     const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(src + head) + i);
     float4 *dst = reinterpret_cast<float4 *>(l + head) + i * (kVec / 4);
@@ -470,58 +505,113 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
       dst[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
   }
-  for (int i = tid; i < n; i += kThreads)
-    if (i < head || i >= head + vecs * kVec) l[i] = put(logit_of(src[i]));
+  if (tid < head) l[tid] = put(logit_of(src[tid]));
+  if (tid < n - head - vecs * kVec) {
+    const int i = head + vecs * kVec + tid;
+    l[i] = put(logit_of(src[i]));
+  }
 
-  Row r{p, s, l, n, first, rank, ctas};
-  r.extremes(lo, hi);
   const float temp = p.temperature ? p.temperature[row] : 1.f;
+  const int top_k = p.top_k ? p.top_k[row] : 0;
+  const float top_p = p.top_p ? p.top_p[row] : 1.f, u = p.u[row], q = p.min_p ? p.min_p[row] : 0.f;
   const bool greedy = !(temp > 0.f);
+  Row r{s, l, n, first, rank, ctas, tid >> 5, tid & 31};
+  r.extremes(lo, hi);
+  auto put_out = [&](int token, float prob) {
+    p.token[row] = token;
+    if (p.prob) p.prob[row] = prob;
+  };
+  if (hi == -INFINITY) {
+    if (rank == 0 && tid == 0) put_out(-1, 0.f);
+    return;
+  }
   if (hi == INFINITY) {  // only those are left, all alike
     for (int i = tid; i < n; i += kThreads) l[i] = l[i] == INFINITY ? 0.f : -INFINITY;
     __syncthreads();
     lo = hi = 0.f;
   }
-  r.w = Weight{hi, greedy, 16. / (0.69314718055994530942 * (double)temp), s.pow16};
-  if (hi == -INFINITY) {
-    if (rank == 0 && tid == 0) {
-      p.token[row] = -1;
-      if (p.prob) p.prob[row] = 0.f;
-    }
-    return;
-  }
-  if (!greedy) {
-    const int top_k = p.top_k ? p.top_k[row] : 0;
-    if (top_k > 0 && top_k < p.V) {
-      const Part t = r.levels(temp, false);
-      if ((uint32_t)top_k < t.count[kLevels]) r.cut_level(top_k, false, temp, lo, t);
-    }
-    const float top_p = p.top_p ? p.top_p[row] : 1.f;
-    if (top_p < 1.f) {
-      const Part t = r.levels(temp, true);
-      const int64_t need = __double2ll_ru((double)top_p * (double)t.mass[kLevels]);
-      r.cut_level((uint64_t)max(need, (int64_t)1), true, temp, lo, t);
-    }
-  }
-  const float q = p.min_p ? p.min_p[row] : 0.f;
+  r.temp = temp;
+  r.lowest = lo;
+  r.w = Weight{hi, fmaxf(__fmaf_rn(-40.f, temp, hi), -FLT_MAX), 16. / (0.69314718055994530942 * (double)temp), s.pow16};
   const double min_w = q > 0.f ? fmin((double)q, 1.) * 0x1p44 : 0.;
-  const float u = p.u[row];
-  uint64_t Z;
-  const int at = r.find(
-      [&](int i, float v) -> uint64_t {
-        if (!r.kept(i, v)) return 0;
-        const double x = r.w(v);
-        return x >= min_w ? Weight::to_fixed(x) : 0;
-      },
-      [&](uint64_t all) -> uint64_t {
-        if (greedy || !(u > 0.f)) return 0;
-        return u < 1.f ? min((uint64_t)((double)u * (double)all), all - 1) : all - 1;
-      },
-      Z);
-  if (at >= 0 && tid == 0) {
-    p.token[row] = first + at;
-    if (p.prob) p.prob[row] = greedy ? 1.f : (float)(r.w(l[at]) / (double)Z);
+  auto target = [&](uint64_t all) -> uint64_t {
+    if (greedy || !(u > 0.f)) return 0;
+    return u < 1.f ? min((uint64_t)((double)u * (double)all), all - 1) : all - 1;
+  };
+  auto need_of = [&](uint64_t all) -> uint64_t {
+    return (uint64_t)max(__double2ll_ru((double)top_p * (double)all), 1ll);
+  };
+
+  // Where the tokens that stay are few and at the top, CTA 0 does the rest from
+  // a list of them: k first tokens, of these those whose mass before them is
+  // below need (0: top_p of the k's), of these what min-p leaves.
+  auto finish = [&](int j, const Levels &t, int k, uint64_t need) {
+    Range top = r.range_of(j, t);
+    top.top = INFINITY;
+    r.gather(top);
+    if (rank != 0) return;
+    const int len = s.list_n, per = Row::threads_each(len), c = tid / per;
+    const Candidate x = s.list[min(c, len - 1)];
+    // the tokens before it, their count above bit 53 (at most 2^8 weights of at most 2^44)
+    const uint64_t ahead = r.over_list(len, per, [&](const Candidate &y) {
+      return y.v > x.v || (y.v == x.v && y.i < x.i) ? y.w | 1ull << 53 : 0;
+    });
+    const uint64_t order = ahead >> 53, before = ahead & ((1ull << 53) - 1);
+    if (c < len && (int)order == min(k, len) - 1) s.found_mass = before + x.w;
+    __syncthreads();
+    if (need == 0) need = top_p < 1.f ? need_of(s.found_mass) : s.found_mass + 1;
+    const bool stays = (int)order < k && before < need && (order == 0 || r.w(x.v) >= min_w);
+    if (c < len && tid % per == 0) s.list[c].w = stays ? x.w : 0;
+    __syncthreads();
+    const uint64_t Z = r.over_list(len, per, [&](const Candidate &y) { return y.w; });
+    const uint64_t below = r.over_list(len, per, [&](const Candidate &y) { return y.i < x.i ? y.w : 0; });
+    const uint64_t at = target(Z);
+    if (c < len && tid % per == 0 && stays && below <= at && at < below + x.w) put_out(x.i, (float)(r.w(x.v) / (double)Z));
+  };
+
+  if (!greedy && top_k > 0 && top_k < p.V) {
+    const Levels t = r.levels<false>();
+    if ((uint32_t)top_k < t.count[kLevels]) {
+      int j = 0;
+      while (t.count[j] < (uint32_t)top_k) ++j;
+      if (t.count[j] <= kList) {
+        finish(j, t, top_k, 0);
+        return;
+      }
+      const Range range = r.range_of(j, t);
+      r.cut(top_k, false, range, t.count[j] - range.above_count);
+    }
   }
+  if (!greedy && top_p < 1.f) {
+    const Levels t = r.levels<true>();
+    const uint64_t need = need_of(t.mass[kLevels]);
+    int j = 0;
+    while (t.mass[j] < need) ++j;
+    if (t.count[j] <= kList) {
+      finish(j, t, kMaxV, need);
+      return;
+    }
+    const Range range = r.range_of(j, t);
+    r.cut(need, true, range, t.count[j] - range.above_count);
+  }
+  uint64_t Z;
+  int at;
+  if (greedy) {
+    at = r.find([&](int, float v) -> uint64_t { return v == hi; }, target, Z);
+  } else if (min_w > 0. || r.last_v > -INFINITY) {
+    // few are kept: the others are seen by their logits, min-p's a little above its bound
+    const float low = min_w > 0. ? fmaxf(r.last_v, __fmaf_rn(temp, logf(fminf(q, 1.f)) * 1.0001f - 1e-4f, hi)) : r.last_v;
+    at = r.find(
+        [&](int i, float v) -> uint64_t {
+          if (!(v >= low && r.kept(i, v))) return 0;
+          const double x = r.w(v);
+          return x >= min_w ? Weight::to_fixed(x) : 0;
+        },
+        target, Z);
+  } else {
+    at = r.find([&](int, float v) { return r.w.fixed(v); }, target, Z);
+  }
+  if (at >= 0 && r.lane == 0) put_out(first + at, greedy ? 1.f : (float)(r.w(l[at]) / (double)Z));
 }
 
 template <class T>
