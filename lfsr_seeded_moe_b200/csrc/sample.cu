@@ -16,9 +16,10 @@ namespace cg = cooperative_groups;
 constexpr int kMaxV = 1 << 18;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 512;
+constexpr int kBins = 4096;
 constexpr int kList = 256;
-constexpr int kLevels = 6;  // and all as the last
+constexpr int kGroups = 128;  // parts of a row whose largest logits are known
+constexpr int kListAt = 96;   // and the one of those, in descending order, from which on a list is made for top-p
 
 struct SampleParams {
   const void *logits;
@@ -72,27 +73,40 @@ struct Weight {
   }
 };
 
-struct Candidate {
-  uint64_t w;
-  float v;
-  int32_t i;
+// A token of a list: its logit in the order of its values, then its index
+// falling, so that of two the larger comes first; and its weight.
+struct alignas(16) Candidate {
+  uint64_t key, w;
+
+  static __device__ __forceinline__ Candidate of(float v, int i, uint64_t w) {
+    const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
+    return Candidate{(uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | ~(uint32_t)i, w};
+  }
+  __device__ __forceinline__ int index() const { return (int)~(uint32_t)key; }
+  __device__ __forceinline__ float logit() const {
+    const uint32_t k = (uint32_t)(key >> 32);
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+  }
 };
 
-struct Shared {
+struct alignas(16) Shared {
   double pow16[16];
-  // what every warp of the row tells every CTA, by turns
-  uint64_t slot[2][kLevels + 1][kMaxCluster * kWarps];
+  // what the CTAs of a row tell one another, by turns
+  uint64_t slot[2][2][kMaxCluster];
+  alignas(16) float group_max[kGroups];
   uint64_t warp_mass[kWarps];
-  uint32_t warp_count[kWarps];
+  float warp_lo[kWarps], warp_hi[kWarps];
+  float m, list_from;
   int32_t list_n;
   int32_t found;
   uint64_t found_mass;
-  uint32_t found_count, found_in;
   union {
     struct {
-      uint32_t count[kBins], lo[kBins], hi[kBins];
+      uint32_t lo[kBins], hi[kBins];
     } hist;
-    Candidate list[kList];
+    struct {
+      Candidate mine[kList], list[kList];  // the CTA's part, and in CTA 0 all
+    };
   };
 };
 
@@ -112,11 +126,10 @@ template <class T> __device__ __forceinline__ T warp_scan_of(T v, int lane) {  /
 
 // The tokens between two logits, in the order of their logits.
 struct Range {
-  float lo, top;   // lo <= v < top
-  float hi;        // the largest v there, or a bound
-  int bin = -1;    // of those, the ones in this bin of [lo, hi], or all
-  uint64_t above_mass = 0;
-  uint32_t above_count = 0;
+  float lo, top;       // lo <= v < top
+  float hi;            // the largest v there, or a bound
+  int bin = -1;        // of those, the ones in this bin of [lo, hi], or all
+  uint64_t above = 0;  // the count or mass of the kept tokens that come before
 
   // Falls from 0 at hi to kBins - 1 at lo, for any lo < hi.
   __device__ __forceinline__ int bin_of(float v) const {
@@ -124,12 +137,6 @@ struct Range {
     return min(kBins - 1, (int)((hi * h - v * h) / (hi * h - lo * h) * kBins));
   }
   __device__ __forceinline__ bool has(float v) const { return v >= lo && v < top && (bin < 0 || bin_of(v) == bin); }
-};
-
-// Counts, and masses, of the tokens with logits from m down to some levels below, and of all.
-struct Levels {
-  uint64_t mass[kLevels + 1];
-  uint32_t count[kLevels + 1];
 };
 
 struct Row {
@@ -140,7 +147,7 @@ struct Row {
   int rank, ctas;  // in the cluster
   int warp, lane;
   int parity = 0;
-  float temp = 1.f, lowest = 0.f;
+  float temp = 1.f;
   Weight w{};
   // the last token that stays, in the order of descending logits and ascending indexes
   float last_v = -INFINITY;
@@ -153,105 +160,98 @@ struct Row {
   // A warp's share of the CTA's logits: contiguous, so that sums over warps are sums over indexes.
   __device__ __forceinline__ int share() const { return ((n + kWarps - 1) / kWarps + 31) & ~31; }
 
-  // f(i, logit) for this thread's logits, four at a time so that their
-  // latencies overlap; i of a place past the end is meaningless, its logit -inf.
-  template <class F> __device__ __forceinline__ void each(F f) const {
-    for (int i = threadIdx.x; i < n; i += 4 * kThreads) {
-      float v[4];
+  // f(i, logit) for this thread's logits, U at a time so that their latencies
+  // overlap; i of a place past the end is meaningless, its logit -inf.
+  template <int U, class F> __device__ __forceinline__ void each(F f) const {
+    for (int i = threadIdx.x; i < n; i += U * kThreads) {
+      float v[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = i + j * kThreads < n ? l[i + j * kThreads] : -INFINITY;
+      for (int j = 0; j < U; ++j) v[j] = i + j * kThreads < n ? l[i + j * kThreads] : -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f(i + j * kThreads, v[j]);
+      for (int j = 0; j < U; ++j) f(i + j * kThreads, v[j]);
     }
   }
 
-  __device__ void sync_row() {
+  __device__ __forceinline__ void sync_row() const {
     if (ctas == 1) __syncthreads();
     else cg::this_cluster().sync();
   }
 
-  // Every warp's values (the same in all its lanes) to every CTA.  Two sets of
+  // A CTA's values, held by its first warp's lanes, to every CTA.  Two sets of
   // slots by turns: who writes one again has passed the barrier after which
   // the others had read it.
-  using Slots = const uint64_t (*)[kMaxCluster * kWarps];
+  using Slots = const uint64_t (*)[kMaxCluster];
   template <int V> __device__ __forceinline__ Slots publish(const uint64_t (&v)[V]) {
     auto slot = s.slot[parity];
     parity ^= 1;
-    if (lane < ctas) {
-      uint64_t *to = ctas == 1 ? &slot[0][0] : cg::this_cluster().map_shared_rank(&slot[0][0], lane);
+    if (threadIdx.x < ctas) {
+      uint64_t *to = ctas == 1 ? &slot[0][0] : cg::this_cluster().map_shared_rank(&slot[0][0], threadIdx.x);
 #pragma unroll
-      for (int j = 0; j < V; ++j) to[j * kMaxCluster * kWarps + rank * kWarps + warp] = v[j];
+      for (int j = 0; j < V; ++j) to[j * kMaxCluster + rank] = v[j];
     }
     sync_row();
     return slot;
   }
 
   // Smallest and largest over the row.
-  __device__ void extremes(float &lo, float &hi) {
+  __device__ __forceinline__ void extremes(float &lo, float &hi) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
+    if (lane == 0) s.warp_lo[warp] = lo, s.warp_hi[warp] = hi;
+    __syncthreads();
+    for (int k = 0; k < kWarps; ++k) lo = fminf(lo, s.warp_lo[k]), hi = fmaxf(hi, s.warp_hi[k]);
     const uint64_t v[1] = {(uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo)};
     const auto slot = publish(v);
-    for (int k = lane; k < ctas * kWarps; k += 32) {
+    for (int k = 0; k < ctas; ++k) {
       lo = fminf(lo, __uint_as_float((uint32_t)slot[0][k]));
       hi = fmaxf(hi, __uint_as_float((uint32_t)(slot[0][k] >> 32)));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
+  }
+
+  // The sum of the warps' values, in the first warp.
+  __device__ __forceinline__ uint64_t cta_sum(const uint64_t (&v)[kWarps]) const {
+    return warp == 0 ? warp_sum_of(lane < kWarps ? v[lane] : 0) : 0;
   }
 
   // The lowest index for which the sum of f up to it exceeds target(the whole
   // sum all), as the position in the CTA that has it, valid in one warp of
   // that CTA; -1 everywhere else.
-  template <class F, class G> __device__ int find(F f, G target, uint64_t &all) {
+  template <class F, class G> __device__ __forceinline__ int find(F f, G target, uint64_t &all) {
     const int per = share();
     auto sum = [&](int lo, int hi) {
       uint64_t a = 0;
-      for (int i = lo + lane; i < hi; i += 128) {
+      for (int i = lo + lane; i < hi; i += 64) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a += f(i + 32 * j, i + 32 * j < hi ? l[i + 32 * j] : -INFINITY);
+        for (int j = 0; j < 2; ++j) a += f(i + 32 * j, i + 32 * j < hi ? l[i + 32 * j] : -INFINITY);
       }
       return warp_sum_of(a);
     };
-    const uint64_t v[1] = {sum(warp * per, min(n, (warp + 1) * per))};
+    uint64_t mine = sum(warp * per, min(n, (warp + 1) * per));
+    if (lane == 0) s.warp_mass[warp] = mine;
+    __syncthreads();
+    const uint64_t v[1] = {cta_sum(s.warp_mass)};
     const auto slot = publish(v);
-    // the warp of the row that has it
-    uint64_t x[kMaxCluster * kWarps / 32];
+    // the CTA that has it, then the warp
+    uint64_t before = 0;
     all = 0;
-#pragma unroll
-    for (int j = 0; j < kMaxCluster * kWarps / 32; ++j) {
-      x[j] = 32 * j + lane < ctas * kWarps ? slot[0][32 * j + lane] : 0;
-      all += x[j];
+    for (int k = 0; k < ctas; ++k) {
+      if (k == rank) before = all;
+      all += slot[0][k];
     }
-    all = warp_sum_of(all);
     uint64_t left = target(all);
-    int at = -1;
-#pragma unroll
-    for (int j = 0; j < kMaxCluster * kWarps / 32; ++j) {
-      const uint64_t upto = warp_scan_of(x[j], lane);
-      const uint32_t over = __ballot_sync(0xffffffffu, upto > left);
-      if (at >= 0) continue;
-      if (over) {
-        const int k = __ffs(over) - 1;
-        at = 32 * j + k;
-        left -= __shfl_sync(0xffffffffu, upto - x[j], k);
-      } else {
-        left -= __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
-    if (at < 0 || at / kWarps != rank) return -1;
-    at %= kWarps;
+    if (left < before || left - before >= slot[0][rank]) return -1;
+    left -= before;
+    int at = 0;
+    while (at < kWarps - 1 && left >= s.warp_mass[at]) left -= s.warp_mass[at++];
     int lo = at * per, hi = min(n, lo + per);
     if (per > 256) {  // all warps on that warp's logits
       const int sub = (per / kWarps + 31) & ~31;
-      const uint64_t c = sum(lo + warp * sub, min(hi, lo + (warp + 1) * sub));
-      if (lane == 0) s.warp_mass[warp] = c;
+      mine = sum(lo + warp * sub, min(hi, lo + (warp + 1) * sub));
+      __syncthreads();
+      if (lane == 0) s.warp_mass[warp] = mine;
       __syncthreads();
       at = 0;
       while (at < kWarps - 1 && left >= s.warp_mass[at]) left -= s.warp_mass[at++];
@@ -268,80 +268,26 @@ struct Row {
     return -1;
   }
 
-  // The levels, in temperatures below m.
-  __device__ __forceinline__ float level(int j) const {
-    constexpr float below[kLevels] = {2.f, 4.f, 6.f, 8.f, 11.f, 15.f};
-    float c = below[0];
-#pragma unroll
-    for (int i = 1; i < kLevels; ++i) c = j == i ? below[i] : c;
-    return __fmaf_rn(-temp, c, w.m);
+  // A token to the CTA's part of the list, which somebody emptied before the
+  // last barrier; what is behind its end is counted only.
+  __device__ __forceinline__ void add_to_list(int i, float v) const {
+    const int at = atomicAdd(&s.list_n, 1);
+    if (at < kList) s.mine[at] = Candidate::of(v, first + i, w.fixed(v));
   }
-  template <bool MASS> __device__ Levels levels() {
-    float at[kLevels];
-#pragma unroll
-    for (int j = 0; j < kLevels; ++j) at[j] = level(j);
-    // a thread has at most 64 logits: its counts stand in bytes, or above bit 51 of its mass, which needs 51
-    uint64_t sum[kLevels + 1] = {};
-    uint32_t bytes[2] = {};
-    each([&](int i, float v) {
-      if (!(v > -INFINITY && kept(i, v))) return;
-      if (MASS) {
-        const uint64_t x = w.fixed(v) | 1ull << 52;
-        sum[kLevels] += x;
-#pragma unroll
-        for (int j = 0; j < kLevels; ++j)
-          if (v >= at[j]) sum[j] += x;
-      } else {
-        bytes[kLevels / 4] += 1u << (8 * (kLevels % 4));
-#pragma unroll
-        for (int j = 0; j < kLevels; ++j)
-          if (v >= at[j]) bytes[j / 4] += 1u << (8 * (j % 4));
-      }
-    });
-    Levels t{};
-    auto add = [&](Slots slot, auto put) {
-#pragma unroll
-      for (int j = 0; j <= kLevels; ++j) {
-        uint64_t a = 0;
-        for (int k = lane; k < ctas * kWarps; k += 32) a += slot[j][k];
-        put(j, warp_sum_of(a));
-      }
-    };
-    if (MASS) {
-      uint64_t v[kLevels + 1];
-#pragma unroll
-      for (int j = 0; j <= kLevels; ++j) {
-        v[j] = warp_sum_of(sum[j] & 0xfffffffffffffull);
-        sum[j] = warp_sum_of((uint32_t)(sum[j] >> 52));
-      }
-      add(publish(v), [&](int j, uint64_t a) { t.mass[j] = a; });
-    } else {
-#pragma unroll
-      for (int j = 0; j <= kLevels; ++j) sum[j] = warp_sum_of(bytes[j / 4] >> (8 * (j % 4)) & 255u);
+  // The parts of all CTAs, of `counts` tokens, together in CTA 0: their number,
+  // and the list if it has room for them.
+  __device__ __forceinline__ int gather(const uint64_t (&counts)[kMaxCluster]) {
+    int total = 0;
+    for (int k = 0; k < ctas; ++k) total += (int)counts[k];
+    if (rank != 0 || total > kList) return total;
+    int c = threadIdx.x, k = 0;
+    if (c < total) {
+      while (c >= (int)counts[k]) c -= (int)counts[k++];
+      const Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, k);
+      s.list[threadIdx.x] = o->mine[c];
     }
-    add(publish(sum), [&](int j, uint64_t a) { t.count[j] = (uint32_t)a; });
-    return t;
-  }
-  // The tokens of level j that are not of the one before.
-  __device__ Range range_of(int j, const Levels &t) const {
-    Range r;
-    r.lo = j < kLevels ? fmaxf(level(j), lowest) : lowest;
-    r.top = j > 0 ? level(j - 1) : INFINITY;
-    r.hi = fminf(r.top, w.m);
-    r.above_mass = j > 0 ? t.mass[j - 1] : 0;
-    r.above_count = j > 0 ? t.count[j - 1] : 0;
-    return r;
-  }
-
-  // The kept tokens of a range, at most kList, in CTA 0's list.
-  __device__ void gather(const Range &r) {
-    if (threadIdx.x == 0) s.list_n = 0;
-    sync_row();
-    Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, 0);
-    each([&](int i, float v) {
-      if (r.has(v) && kept(i, v)) o->list[atomicAdd(&o->list_n, 1)] = Candidate{w.fixed(v), v, first + i};
-    });
-    sync_row();
+    __syncthreads();
+    return total;
   }
   // The sum of f over the list, in each of `per` threads.
   template <class F> __device__ __forceinline__ uint64_t over_list(int n, int per, F f) {
@@ -355,115 +301,149 @@ struct Row {
   __device__ __forceinline__ static int threads_each(int n) { return n <= 64 ? 8 : n <= 128 ? 4 : 2; }
 
   // Sets the last token that stays to the one at which the kept tokens' count
-  // (by_mass: their mass), in their order, first reaches `need`, which is in
-  // the range of `in` tokens.
-  __device__ void cut(uint64_t need, bool by_mass, Range r, uint32_t in) {
+  // (by_mass: their mass), in their order, first reaches `need`.  r: where it
+  // is, from its top down to where weights are 0; kept tokens that are too few
+  // to reach need all stay.
+  __device__ __forceinline__ void cut(uint64_t need, bool by_mass, Range r) {
     auto inside = [&](int i, float v) { return r.has(v) && kept(i, v); };
-    while (in > kList && r.lo < r.hi) {
+    while (r.lo < r.hi) {
       // a histogram of the range; the bin that has the token is the next range
       __syncthreads();
-      for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist.count[b] = s.hist.lo[b] = s.hist.hi[b] = 0;
+      for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist.lo[b] = s.hist.hi[b] = 0;
       __syncthreads();
-      each([&](int i, float v) {
+      each<2>([&](int i, float v) {
         if (!inside(i, v)) return;
         const int b = r.bin_of(v);
-        atomicAdd(&s.hist.count[b], 1u);
         if (by_mass) {
           const uint64_t x = w.fixed(v);
           const uint32_t lo = (uint32_t)x, old = atomicAdd(&s.hist.lo[b], lo);
-          atomicAdd(&s.hist.hi[b], (uint32_t)(x >> 32) + (old + lo < lo ? 1u : 0u));
+          const uint32_t hi = (uint32_t)(x >> 32) + (old + lo < lo ? 1u : 0u);
+          if (hi) atomicAdd(&s.hist.hi[b], hi);
+        } else {
+          atomicAdd(&s.hist.lo[b], 1u);
         }
       });
       sync_row();
-      // every CTA adds all histograms and finds the bin
+      // each CTA adds its part of all histograms
       constexpr int kPer = kBins / kThreads;
-      uint64_t mass[kPer], m = 0;
-      uint32_t count[kPer], c = 0;
+      const int per = kPer / ctas, b0 = rank * (kBins / ctas) + threadIdx.x * per;
+      uint64_t x[kPer] = {}, sum = 0;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        const int b = threadIdx.x * kPer + q;
-        mass[q] = 0, count[q] = 0;
+        if (q >= per) break;
         for (int k = 0; k < ctas; ++k) {
           const Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, k);
-          count[q] += o->hist.count[b];
-          if (by_mass) mass[q] += ((uint64_t)o->hist.hi[b] << 32) + o->hist.lo[b];
+          x[q] += ((uint64_t)o->hist.hi[b0 + q] << 32) + o->hist.lo[b0 + q];
         }
-        m += mass[q], c += count[q];
+        sum += x[q];
       }
-      uint64_t ms = warp_scan_of(m, lane);
-      uint32_t cs = warp_scan_of(c, lane);
-      if (lane == 31) s.warp_mass[warp] = ms, s.warp_count[warp] = cs;
+      uint64_t upto = warp_scan_of(sum, lane);
+      if (lane == 31) s.warp_mass[warp] = upto;
       __syncthreads();
-      ms += r.above_mass - m, cs += r.above_count - c;
-      for (int k = 0; k < warp; ++k) ms += s.warp_mass[k], cs += s.warp_count[k];
+      const uint64_t v[1] = {cta_sum(s.warp_mass)};
+      const auto part = publish(v);
+      uint64_t all = 0;
+      upto += r.above - sum;
+      for (int k = 0; k < ctas; ++k) {
+        if (k < rank) upto += part[0][k];
+        all += part[0][k];
+      }
+      if (r.above + all < need) return;
+      for (int k = 0; k < warp; ++k) upto += s.warp_mass[k];
+      if (threadIdx.x == 0) s.found = -1, s.list_n = 0;
+      __syncthreads();
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        const uint64_t from = by_mass ? ms : cs, to = from + (by_mass ? mass[q] : count[q]);
-        if (from < need && need <= to)
-          s.found = threadIdx.x * kPer + q, s.found_mass = ms, s.found_count = cs, s.found_in = count[q];
-        ms += mass[q], cs += count[q];
+        if (q >= per) break;
+        if (upto < need && need <= upto + x[q]) s.found = b0 + q, s.found_mass = upto;
+        upto += x[q];
       }
       __syncthreads();
-      r.bin = s.found;
-      r.above_mass = s.found_mass;
-      r.above_count = s.found_count;
-      in = s.found_in;
-      if (in <= kList) break;
-      // its logits' smallest and largest
+      const uint64_t mine[2] = {(uint64_t)(s.found + 1), s.found >= 0 ? s.found_mass : 0};
+      const auto found = publish(mine);
+      uint64_t bin = 0, above = 0;
+      for (int k = 0; k < ctas; ++k) bin += found[0][k], above += found[1][k];
+      r.bin = (int)bin - 1;
+      r.above = above;
+      if (order(need, by_mass, r)) return;
+      // too many: from their largest to their smallest logit
       float lo = INFINITY, hi = -INFINITY;
-      each([&](int i, float v) {
+      each<4>([&](int i, float v) {
         if (inside(i, v)) lo = fminf(lo, v), hi = fmaxf(hi, v);
       });
       extremes(lo, hi);
       r.lo = lo, r.hi = hi, r.bin = -1;
       r.top = nextafterf(hi, INFINITY);
     }
-    uint64_t found[1] = {0};  // the token's index and logit
-    if (in <= kList) {
-      gather(r);
-      if (rank == 0) {  // few enough: CTA 0 orders them
-        const int len = s.list_n, per = threads_each(len), c = threadIdx.x / per;
-        const Candidate x = s.list[min(c, len - 1)];
-        const uint64_t before = (by_mass ? r.above_mass : r.above_count) + over_list(len, per, [&](const Candidate &y) {
-          return y.v > x.v || (y.v == x.v && y.i < x.i) ? (by_mass ? y.w : 1) : 0;
-        });
-        if (c < len && before < need && need <= before + (by_mass ? x.w : 1))
-          s.found_mass = (uint64_t)__float_as_uint(x.v) << 32 | (uint32_t)x.i;
-        __syncthreads();
-        found[0] = s.found_mass;
-      }
-      const uint64_t x = publish(found)[0][0];
-      last_v = __uint_as_float((uint32_t)(x >> 32));
-      last_i = (int)(uint32_t)x;
-    } else {
-      // equal logits: by their indexes
-      const float v = r.lo;
-      uint64_t rest = need - (by_mass ? r.above_mass : r.above_count);
-      if (by_mass) {
-        const uint64_t x = w.fixed(v);
-        rest = (rest + x - 1) / x;
-      }
-      uint64_t all;
-      const int at = find([&](int i, float y) -> uint64_t { return y == v && kept(i, y); },
-                          [&](uint64_t) { return rest - 1; }, all);
-      found[0] = at >= 0 ? first + at + 1 : 0;  // in one warp of the row
-      const auto slot = publish(found);
-      uint64_t a = 0;
-      for (int k = lane; k < ctas * kWarps; k += 32) a += slot[0][k];
-      last_v = v;
-      last_i = (int)warp_sum_of(a) - 1;
+    // equal logits: by their indexes
+    const float v = r.lo;
+    uint64_t rest = need - r.above, all;
+    if (by_mass) {
+      const uint64_t x = w.fixed(v);
+      rest = (rest + x - 1) / x;
     }
+    const int at = find([&](int i, float y) -> uint64_t { return y == v && kept(i, y); },
+                        [&](uint64_t) { return rest - 1; }, all);
+    if (all < rest) return;
+    __syncthreads();
+    if (threadIdx.x == 0) s.found = 0;
+    __syncthreads();
+    if (at >= 0 && lane == 0) s.found = first + at + 1;  // in one warp of the row
+    __syncthreads();
+    const uint64_t found[1] = {(uint64_t)s.found};
+    const auto slot = publish(found);
+    last_v = v;
+    last_i = -1;
+    for (int k = 0; k < ctas; ++k) last_i += (int)slot[0][k];
+  }
+
+  // cut() for a range whose tokens fit the list (emptied before the last
+  // barrier); false if they do not.
+  __device__ __forceinline__ bool order(uint64_t need, bool by_mass, const Range &r) {
+    each<4>([&](int i, float v) {
+      if (r.has(v) && kept(i, v)) add_to_list(i, v);
+    });
+    __syncthreads();
+    const uint64_t count[1] = {(uint64_t)s.list_n};
+    const int len = gather(publish(count)[0]);
+    uint64_t found[1] = {0};  // the token's key
+    if (rank == 0 && len <= kList) {
+      const int per = threads_each(len), c = threadIdx.x / per;
+      const Candidate x = s.list[min(c, len - 1)];
+      const uint64_t before =
+          r.above + over_list(len, per, [&](const Candidate &y) { return y.key > x.key ? (by_mass ? y.w : 1) : 0; });
+      if (c < len && before < need && need <= before + (by_mass ? x.w : 1)) s.found_mass = x.key;
+      __syncthreads();
+      found[0] = s.found_mass;
+    }
+    const auto slot = publish(found);
+    if (!slot[0][0]) return false;
+    const Candidate last{slot[0][0], 0};
+    last_v = last.logit();
+    last_i = last.index();
+    return true;
   }
 };
 
+// cut() apart from the code that most rows run.  The row goes by value, so that
+// its caller's stays in registers.
+struct Last {
+  float v;
+  int i, parity;
+};
+__device__ __noinline__ Last cut_row(Row r, uint64_t need, bool by_mass, Range range) {
+  r.cut(need, by_mass, range);
+  return Last{r.last_v, r.last_i, r.parity};
+}
+
 // NaN is never drawn.
-__device__ __forceinline__ float logit_of(float v) { return v == v ? v : -INFINITY; }
+__device__ __forceinline__ float logit_of(float v) { return fmaxf(v, -INFINITY); }
 __device__ __forceinline__ float logit_of(__nv_bfloat16 v) { return logit_of(__bfloat162float(v)); }
 
 template <class T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
-  extern __shared__ float4 s_logits[];
-  __shared__ Shared s;
+  extern __shared__ float4 smem[];
+  Shared &s = *reinterpret_cast<Shared *>(smem);
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / ctas, tid = threadIdx.x;
@@ -476,11 +456,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const T *src = reinterpret_cast<const T *>(p.logits) + (size_t)row * p.ld + first;
   constexpr int kVec = 16 / sizeof(T);
   const int head = min(n, (int)((-(uintptr_t)src & 15) / sizeof(T)));
-  float *l = reinterpret_cast<float *>(s_logits) + (-head & 3);
-  float lo = INFINITY, hi = -INFINITY;
+  float *l = reinterpret_cast<float *>(&s + 1) + (-head & 3);
+  float hi = -INFINITY;
   auto put = [&](float v) {
     hi = fmaxf(hi, v);
-    if (v > -INFINITY) lo = fminf(lo, v);
     return v;
   };
   const int vecs = (n - head) / kVec;
@@ -514,9 +493,47 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const float temp = p.temperature ? p.temperature[row] : 1.f;
   const int top_k = p.top_k ? p.top_k[row] : 0;
   const float top_p = p.top_p ? p.top_p[row] : 1.f, u = p.u[row], q = p.min_p ? p.min_p[row] : 0.f;
-  const bool greedy = !(temp > 0.f);
+  const bool greedy = !(temp > 0.f), by_count = !greedy && top_k > 0 && top_k < p.V, by_mass = !greedy && top_p < 1.f;
   Row r{s, l, n, first, rank, ctas, tid >> 5, tid & 31};
-  r.extremes(lo, hi);
+
+  // The largest logits of kGroups parts of the row, in every CTA: `width` threads have one.
+  const int width = kThreads / kGroups * ctas;
+  for (int o = 1; o < width; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  if (tid % width < ctas) {
+    float *to = ctas == 1 ? s.group_max : cluster.map_shared_rank(s.group_max, tid % width);
+    to[rank * (kGroups / ctas) + tid / width] = hi;
+  }
+  if (tid == 0) s.list_n = 0;
+  r.sync_row();
+  // k of them reach the k-th, so k tokens do, and seldom many more: a list from
+  // there on has a top-k, and of most rows a top-p
+  if (by_count || by_mass) {
+    const int at = by_count ? min(top_k, kListAt) : kListAt;
+    constexpr int kShare = kThreads / kGroups;  // neighbouring threads share a part's comparisons
+    const int c = tid / kShare;
+    const float x = s.group_max[c];
+    int order = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / 4 / kShare; ++j) {
+      const int at4 = (j * kShare + tid % kShare) * 4;
+      const float4 y = *reinterpret_cast<const float4 *>(s.group_max + at4);
+      order += (y.x > x) | ((y.x == x) & (at4 < c));
+      order += (y.y > x) | ((y.y == x) & (at4 + 1 < c));
+      order += (y.z > x) | ((y.z == x) & (at4 + 2 < c));
+      order += (y.w > x) | ((y.w == x) & (at4 + 3 < c));
+    }
+#pragma unroll
+    for (int o = 1; o < kShare; o <<= 1) order += __shfl_xor_sync(0xffffffffu, order, o);
+    if (order == 0) s.m = x;
+    if (order == at - 1) s.list_from = x;
+    __syncthreads();
+    hi = s.m;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kGroups / 32; ++j) hi = fmaxf(hi, s.group_max[32 * j + r.lane]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
   auto put_out = [&](int token, float prob) {
     p.token[row] = token;
     if (p.prob) p.prob[row] = prob;
@@ -525,13 +542,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (rank == 0 && tid == 0) put_out(-1, 0.f);
     return;
   }
-  if (hi == INFINITY) {  // only those are left, all alike
+  const bool infinite = hi == INFINITY;
+  if (infinite) {  // only those are left, all alike
     for (int i = tid; i < n; i += kThreads) l[i] = l[i] == INFINITY ? 0.f : -INFINITY;
     __syncthreads();
-    lo = hi = 0.f;
+    hi = 0.f;
   }
   r.temp = temp;
-  r.lowest = lo;
   r.w = Weight{hi, fmaxf(__fmaf_rn(-40.f, temp, hi), -FLT_MAX), 16. / (0.69314718055994530942 * (double)temp), s.pow16};
   const double min_w = q > 0.f ? fmin((double)q, 1.) * 0x1p44 : 0.;
   auto target = [&](uint64_t all) -> uint64_t {
@@ -542,57 +559,109 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     return (uint64_t)max(__double2ll_ru((double)top_p * (double)all), 1ll);
   };
 
-  // Where the tokens that stay are few and at the top, CTA 0 does the rest from
-  // a list of them: k first tokens, of these those whose mass before them is
-  // below need (0: top_p of the k's), of these what min-p leaves.
-  auto finish = [&](int j, const Levels &t, int k, uint64_t need) {
-    Range top = r.range_of(j, t);
-    top.top = INFINITY;
-    r.gather(top);
-    if (rank != 0) return;
-    const int len = s.list_n, per = Row::threads_each(len), c = tid / per;
-    const Candidate x = s.list[min(c, len - 1)];
-    // the tokens before it, their count above bit 53 (at most 2^8 weights of at most 2^44)
-    const uint64_t ahead = r.over_list(len, per, [&](const Candidate &y) {
-      return y.v > x.v || (y.v == x.v && y.i < x.i) ? y.w | 1ull << 53 : 0;
-    });
-    const uint64_t order = ahead >> 53, before = ahead & ((1ull << 53) - 1);
-    if (c < len && (int)order == min(k, len) - 1) s.found_mass = before + x.w;
-    __syncthreads();
-    if (need == 0) need = top_p < 1.f ? need_of(s.found_mass) : s.found_mass + 1;
-    const bool stays = (int)order < k && before < need && (order == 0 || r.w(x.v) >= min_w);
-    if (c < len && tid % per == 0) s.list[c].w = stays ? x.w : 0;
-    __syncthreads();
-    const uint64_t Z = r.over_list(len, per, [&](const Candidate &y) { return y.w; });
-    const uint64_t below = r.over_list(len, per, [&](const Candidate &y) { return y.i < x.i ? y.w : 0; });
-    const uint64_t at = target(Z);
-    if (c < len && tid % per == 0 && stays && below <= at && at < below + x.w) put_out(x.i, (float)(r.w(x.v) / (double)Z));
-  };
-
-  if (!greedy && top_k > 0 && top_k < p.V) {
-    const Levels t = r.levels<false>();
-    if ((uint32_t)top_k < t.count[kLevels]) {
-      int j = 0;
-      while (t.count[j] < (uint32_t)top_k) ++j;
-      if (t.count[j] <= kList) {
-        finish(j, t, top_k, 0);
-        return;
-      }
-      const Range range = r.range_of(j, t);
-      r.cut(top_k, false, range, t.count[j] - range.above_count);
+  uint64_t all_mass = 0, list_mass = 0;  // of the row, and from list_from on
+  float list_from = INFINITY;
+  if (by_count || by_mass) {
+    const float from = p.V <= kList || infinite ? -FLT_MAX : fmaxf(s.list_from, -FLT_MAX);
+    uint64_t sum[2] = {0, 0};
+    if (by_count) {
+      r.each<4>([&](int i, float v) {
+        if (v >= from) r.add_to_list(i, v);
+      });
+    } else {
+      r.each<2>([&](int i, float v) {
+        sum[0] += r.w.fixed(v);
+        if (v >= from) r.add_to_list(i, v);
+      });
+      sum[0] = warp_sum_of(sum[0]);
+      if (r.lane == 0) s.warp_mass[r.warp] = sum[0];
     }
-  }
-  if (!greedy && top_p < 1.f) {
-    const Levels t = r.levels<true>();
-    const uint64_t need = need_of(t.mass[kLevels]);
-    int j = 0;
-    while (t.mass[j] < need) ++j;
-    if (t.count[j] <= kList) {
-      finish(j, t, kMaxV, need);
+    __syncthreads();
+    if (!by_count) sum[0] = r.cta_sum(s.warp_mass);
+    sum[1] = (uint64_t)s.list_n;
+    const auto slot = r.publish(sum);
+    const int len = r.gather(slot[1]), per = Row::threads_each(len), c = tid / per;
+    for (int k = 0; k < ctas; ++k) all_mass += slot[0][k];
+    // CTA 0 puts the list in order: a token's place, and the mass before it
+    uint64_t good[2] = {0, 0}, need = 0, before = 0;
+    int order = kList;
+    Candidate x{};
+    float v = 0.f;
+    if (rank == 0 && len <= kList) {
+      x = s.list[min(c, len - 1)];
+      v = x.logit();
+      // their count above bit 53 (at most 2^8 weights of at most 2^44)
+      const uint64_t ahead = r.over_list(len, per, [&](const Candidate &y) {
+        return y.key > x.key ? y.w | 1ull << 53 : 0;
+      });
+      if (c < len) order = (int)(ahead >> 53);
+      before = ahead & ((1ull << 53) - 1);
+      if (order == (by_count ? min(top_k, len) : len) - 1) s.found_mass = before + x.w;
+      if (order == len - 1) s.found = r.w(v) < min_w || p.V <= kList;
+      __syncthreads();
+      // all that stays is in the list if its end is behind top-k's, top-p's or min-p's
+      const bool whole = s.found || (by_count && len >= top_k);
+      need = by_mass ? need_of(by_count ? s.found_mass : all_mass) : s.found_mass + 1;
+      good[0] = by_count ? whole && (!by_mass || len >= top_k || p.V <= kList) : whole || s.found_mass >= need;
+      good[1] = s.found_mass;
+    }
+    const auto told = r.publish(good);
+    list_from = told[1][0] && !by_count ? from : INFINITY;
+    list_mass = told[1][0];
+    if (told[0][0]) {
+      if (rank != 0) return;
+      // tokens that stay: of the first top_k, those with less than need before them that min-p leaves
+      const bool stays = c < len && order < (by_count ? top_k : kList) && before < need && (order == 0 || r.w(v) >= min_w);
+      if (c < len && tid % per == 0) s.list[c].w = stays ? x.w : 0;
+      __syncthreads();
+      uint64_t Z = 0, below = 0;
+#pragma unroll 4
+      for (int j = tid & (per - 1); j < len; j += per) {
+        const Candidate y = s.list[j];
+        Z += y.w;
+        below += (uint32_t)y.key > (uint32_t)x.key ? y.w : 0;
+      }
+      for (int o = 1; o < per; o <<= 1) {
+        Z += __shfl_xor_sync(0xffffffffu, Z, o);
+        below += __shfl_xor_sync(0xffffffffu, below, o);
+      }
+      const uint64_t at = target(Z);
+      if (tid % per == 0 && stays && below <= at && at < below + x.w) put_out(x.index(), (float)(r.w(v) / (double)Z));
       return;
     }
-    const Range range = r.range_of(j, t);
-    r.cut(need, true, range, t.count[j] - range.above_count);
+  }
+  if (by_count || by_mass) {
+    // the slow way: down to 32 temperatures below m, where weights are 0
+    Range range;
+    range.lo = fmaxf(__fmaf_rn(-32.f, temp, hi), -FLT_MAX);
+    range.top = INFINITY;
+    range.hi = hi;
+    auto cut = [&](uint64_t need, bool mass) {
+      const Last last = cut_row(r, need, mass, range);
+      r.last_v = last.v, r.last_i = last.i, r.parity = last.parity;
+    };
+    if (by_count) {
+      cut(top_k, false);
+      if (by_mass) {
+        uint64_t sum[1] = {0};
+        r.each<2>([&](int i, float v) {
+          if (v >= r.last_v && r.kept(i, v)) sum[0] += r.w.fixed(v);
+        });
+        sum[0] = warp_sum_of(sum[0]);
+        __syncthreads();
+        if (r.lane == 0) s.warp_mass[r.warp] = sum[0];
+        __syncthreads();
+        sum[0] = r.cta_sum(s.warp_mass);
+        const auto slot = r.publish(sum);
+        all_mass = 0;
+        for (int k = 0; k < ctas; ++k) all_mass += slot[0][k];
+      }
+    } else if (list_from < INFINITY) {  // below the list, whose mass is known
+      range.top = range.hi = list_from;
+      range.lo = fminf(range.lo, list_from);
+      range.above = list_mass;
+    }
+    if (by_mass) cut(need_of(all_mass), true);
   }
   uint64_t Z;
   int at;
@@ -623,7 +692,7 @@ int32_t launch_sample(SampleParams p, int32_t B, cudaStream_t s) {
                                 ((int64_t)B * ctas * 2 <= 2 * num_sms() && p.V / (2 * ctas) >= 2048)))
     ctas *= 2;
   p.len = ceil_div(ceil_div(p.V, ctas), 8) * 8;
-  const size_t smem = (size_t)(p.len + 8) * 4;
+  const size_t smem = sizeof(Shared) + (size_t)(p.len + 8) * 4;
   auto k = sample_kernel<T>;
   if (int32_t st = ensure_smem((const void *)k, smem)) return st;
   cudaLaunchConfig_t cfg{};
