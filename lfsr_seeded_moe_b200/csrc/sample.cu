@@ -131,10 +131,25 @@ struct Range {
   int bin = -1;        // of those, the ones in this bin of [lo, hi], or all
   uint64_t above = 0;  // the count or mass of the kept tokens that come before
 
-  // Falls from 0 at hi to kBins - 1 at lo, for any lo < hi.
+  // Falls from 0 at hi to kBins - 1 at lo, for any lo < hi: where hi - lo is so
+  // small that `scale` is infinite, hi is in bin 0 and all others in the last.
+  float half = 1.f, scale = 0.f;
+  __device__ __forceinline__ void set_bins() {
+    half = hi - lo < INFINITY ? 1.f : 0.5f;
+    scale = kBins / (hi * half - lo * half);
+    bin = -1;
+  }
   __device__ __forceinline__ int bin_of(float v) const {
-    const float h = hi - lo < INFINITY ? 1.f : 0.5f;
-    return min(kBins - 1, (int)((hi * h - v * h) / (hi * h - lo * h) * kBins));
+    return min(kBins - 1, (int)(__fmaf_rn(-half, v, hi * half) * scale));
+  }
+  // The chosen bin's tokens lie between lo and top too; these are bounds that
+  // are a little wide, to see most others without their bin.
+  __device__ __forceinline__ void set_bin(int b) {
+    bin = b;
+    if (!(scale < 1e30f)) return;  // the bounds themselves would be rounded away
+    const float eps = 0x1p-20f * (fabsf(hi) + fabsf(lo)) * half, of = hi * half, width = 1.f / scale;
+    lo = fmaxf(lo, (of - ((b + 1.01f) * width + eps)) / half);
+    if (b > 0) top = fminf(top, (of - ((b - 0.01f) * width - eps)) / half);
   }
   __device__ __forceinline__ bool has(float v) const { return v >= lo && v < top && (bin < 0 || bin_of(v) == bin); }
 };
@@ -308,6 +323,7 @@ struct Row {
     auto inside = [&](int i, float v) { return r.has(v) && kept(i, v); };
     while (r.lo < r.hi) {
       // a histogram of the range; the bin that has the token is the next range
+      r.set_bins();
       __syncthreads();
       for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist.lo[b] = s.hist.hi[b] = 0;
       __syncthreads();
@@ -331,7 +347,9 @@ struct Row {
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
         if (q >= per) break;
-        for (int k = 0; k < ctas; ++k) {
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+          if (k >= ctas) break;
           const Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, k);
           x[q] += ((uint64_t)o->hist.hi[b0 + q] << 32) + o->hist.lo[b0 + q];
         }
@@ -363,7 +381,7 @@ struct Row {
       const auto found = publish(mine);
       uint64_t bin = 0, above = 0;
       for (int k = 0; k < ctas; ++k) bin += found[0][k], above += found[1][k];
-      r.bin = (int)bin - 1;
+      r.set_bin((int)bin - 1);
       r.above = above;
       if (order(need, by_mass, r)) return;
       // too many: from their largest to their smallest logit
