@@ -1,16 +1,22 @@
 // balance.cu -- nslm_moe_balance and nslm_moe_balance_grad: the experts' counts
 // and the load-balance loss of a router, and the loss's gradient.
 #include <algorithm>
+#include <type_traits>
+
+#include <cooperative_groups.h>
 
 #include "common.cuh"
 
 namespace nslm {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kMaxE = 1024;
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCtas = 296;
-constexpr int kOneLaunchT = 1024;  // up to here one CTA, and no workspace
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kOneLaunchT = 1024;  // up to here one cluster does it all, and there is no workspace
+constexpr int kMaxCtas = 296;      // CTAs that leave parts in the workspace
 
 struct BalanceParams {
   const float *logits;
@@ -22,142 +28,304 @@ struct BalanceParams {
   float *mean_p, *loss;
   float *part_p;    // [CTAs][E]
   int32_t *part_c;  // [CTAs][E + 1]
+  int32_t parts;
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ float warp_add(float v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+// LANES neighbouring lanes have a token, NV of its logits each: fours of
+// neighbours where E is a multiple of 4 (VEC), else every LANES-th.  A token's
+// softmax is then a few shuffles away, and a lane keeps its columns' sums in
+// registers over all its tokens.
+template <int LANES, int NV, bool VEC> struct Token {
+  static constexpr int kNV = NV;
+  static constexpr int kTokens = 32 / LANES;  // of a warp
 
-// Every warp adds the softmax of its tokens to a shared row of its own.
-__device__ void count_tokens(const BalanceParams &p, float *s_p, int32_t *s_c) {
+  static __device__ __forceinline__ int lane() { return threadIdx.x & (LANES - 1); }
+  static __device__ __forceinline__ int column(int j) {
+    return VEC ? (lane() + LANES * (j / 4)) * 4 + j % 4 : lane() + LANES * j;
+  }
+  // -inf past the end
+  static __device__ __forceinline__ void load(float (&z)[NV], const float *row, int E) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < NV; j += 4) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (column(j) < E) v = *reinterpret_cast<const float4 *>(row + column(j));
+        z[j] = v.x, z[j + 1] = v.y, z[j + 2] = v.z, z[j + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) z[j] = column(j) < E ? row[column(j)] : -INFINITY;
+    }
+  }
+  static __device__ __forceinline__ void store(float *row, const float (&z)[NV], int E) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < NV; j += 4)
+        if (column(j) < E) *reinterpret_cast<float4 *>(row + column(j)) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (column(j) < E) row[column(j)] = z[j];
+    }
+  }
+  static __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  // exp(z - max), in place; a token whose logits are all -inf has zeros, NaN stays NaN
+  static __device__ __forceinline__ void exps(float (&z)[NV]) {
+    float m = z[0];
+#pragma unroll
+    for (int j = 1; j < NV; ++j) m = fmaxf(m, z[j]);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) z[j] = expf(z[j] - from);
+  }
+};
+
+// The CTA's tokens of a grid of `ctas`: the probabilities' sums to s_p[E], the
+// counts and the number of tokens to s_c[E + 1].  s_w: kWarps x E.
+template <class Tok> __device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, int ctas, float *s_w, float *s_p, int32_t *s_c) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < kWarps * p.E; i += kThreads) s_p[i] = 0.f;
   for (int i = tid; i <= p.E; i += kThreads) s_c[i] = 0;
   __syncthreads();
-  for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
+  int n = 0;
+  for (int t = cta * kThreads + tid; t < p.T; t += ctas * kThreads) {
     if (p.mask && p.mask[t] == 0) continue;
-    const float *z = p.logits + (size_t)t * p.E;
-    float m = -INFINITY, d = 0.f;
-    bool nan = false;
-    for (int e = lane; e < p.E; e += 32) m = fmaxf(m, z[e]), nan |= z[e] != z[e];
-    m = warp_max(m);
-    if (__any_sync(0xffffffffu, nan)) m = NAN;
-    if (m != -INFINITY) {
-      for (int e = lane; e < p.E; e += 32) d += expf(z[e] - m);
-      d = warp_add(d);
-      for (int e = lane; e < p.E; e += 32) s_p[warp * p.E + e] += expf(z[e] - m) / d;
-    }
-    if (lane < p.k) {
-      const int e = p.ids[(size_t)t * p.k + lane];
+    ++n;
+    for (int q = 0; q < p.k; ++q) {
+      const int e = p.ids[(size_t)t * p.k + q];
       if (e >= 0 && e < p.E) atomicAdd(&s_c[e], 1);
     }
-    if (lane == 0) atomicAdd(&s_c[p.E], 1);
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) atomicAdd(&s_c[p.E], n);
+  float acc[Tok::kNV] = {};
+  constexpr int kRows = Tok::kTokens * kWarps;
+  for (int t0 = cta * kRows; t0 < p.T; t0 += ctas * kRows) {
+    const int t = t0 + tid / (32 / Tok::kTokens);
+    const bool live = t < p.T && (!p.mask || p.mask[t] != 0);
+    float z[Tok::kNV];
+#pragma unroll
+    for (int j = 0; j < Tok::kNV; ++j) z[j] = -INFINITY;
+    if (live) Tok::load(z, p.logits + (size_t)t * p.E, p.E);
+    Tok::exps(z);
+    float d = 0.f;
+#pragma unroll
+    for (int j = 0; j < Tok::kNV; ++j) d += z[j];
+    d = Tok::sum(d);
+    const float r = d == 0.f ? 0.f : 1.f / d;  // nothing left in the row: nothing to add
+#pragma unroll
+    for (int j = 0; j < Tok::kNV; ++j) acc[j] = fmaf(z[j], r, acc[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < Tok::kNV; ++j) {
+#pragma unroll
+    for (int o = 32 / Tok::kTokens; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+    if (lane < 32 / Tok::kTokens && Tok::column(j) < p.E) s_w[warp * p.E + Tok::column(j)] = acc[j];
   }
   __syncthreads();
-}
-
-__device__ void finish(const BalanceParams &p, int ctas) {
-  __shared__ int32_t s_n;
-  __shared__ double s_sum[kThreads];
-  const int tid = threadIdx.x;
-  for (int e = tid; e <= p.E; e += kThreads) {
-    int c = 0;
-    for (int g = 0; g < ctas; ++g) c += p.part_c[(size_t)g * (p.E + 1) + e];
-    p.counts[e] = c;
-    if (e == p.E) s_n = c;
-  }
-  __syncthreads();
-  const double n = max(1, s_n);
-  double sum = 0;
   for (int e = tid; e < p.E; e += kThreads) {
-    double q = 0;
-    for (int g = 0; g < ctas; ++g) q += p.part_p[(size_t)g * p.E + e];
-    q /= n;
-    if (p.mean_p) p.mean_p[e] = (float)q;
-    sum += q * p.counts[e];
-  }
-  s_sum[tid] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kThreads; ++i) sum += s_sum[i];
-    p.loss[0] = (float)(sum * p.coef * p.E / (p.k * n));
-    if (p.offsets) {
-      int c = 0;
-      for (int e = 0; e <= p.E; ++e) {
-        p.offsets[e] = c;
-        if (e < p.E) c += p.counts[e];
-      }
-    }
-  }
-}
-
-// Few tokens: one CTA does it all, with the sums in shared memory.
-__global__ void __launch_bounds__(kThreads) balance_one_kernel(BalanceParams p) {
-  extern __shared__ float s_p[];
-  int32_t *s_c = reinterpret_cast<int32_t *>(s_p + kWarps * p.E);
-  count_tokens(p, s_p, s_c);
-  for (int e = threadIdx.x; e < p.E; e += kThreads)
-    for (int w = 1; w < kWarps; ++w) s_p[e] += s_p[w * p.E + e];
-  __syncthreads();
-  p.part_p = s_p;
-  p.part_c = s_c;
-  finish(p, 1);
-}
-
-__global__ void __launch_bounds__(kThreads) balance_part_kernel(const BalanceParams p) {
-  extern __shared__ float s_p[];
-  int32_t *s_c = reinterpret_cast<int32_t *>(s_p + kWarps * p.E);
-  count_tokens(p, s_p, s_c);
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
     float q = 0;
-    for (int w = 0; w < kWarps; ++w) q += s_p[w * p.E + e];
-    p.part_p[(size_t)blockIdx.x * p.E + e] = q;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) q += s_w[w * p.E + e];
+    s_p[e] = q;
   }
+}
+
+struct Finish {
+  double sum[kThreads];
+  int32_t count[kThreads];
+  int32_t slice[kMaxE / kCluster + 1];
+  double loss[kCluster];
+  int32_t base[kCluster];
+};
+
+// The end, by a cluster whose CTAs have a slice of the experts each: part(g, e)
+// and tokens(g, e) give the sums and counts of g's tokens, e = E their number.
+template <class P, class C> __device__ void finish(const BalanceParams &p, Finish &s, int parts, P part, C tokens) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
+  const int e0 = p.E * rank / kCluster, len = p.E * (rank + 1) / kCluster - e0;
+  // a column for each expert of the slice, and one for the number of tokens
+  const int cols = len + 1, sets = kThreads / cols, set = tid / cols, c = tid - set * cols;
+  const int e = c < len ? e0 + c : p.E;
+  double q = 0;
+  int n = 0;
+  if (set < sets)
+    for (int g = set; g < parts; g += sets) {
+      if (c < len) q += part(g, e);
+      n += tokens(g, e);
+    }
+  s.sum[tid] = q;
+  s.count[tid] = n;
+  __syncthreads();
+  if (set == 0) {
+    for (int i = 1; i < sets; ++i) q += s.sum[i * cols + c], n += s.count[i * cols + c];
+    s.slice[c] = n;
+    s.sum[c] = q;
+  }
+  __syncthreads();
+  const int live = s.slice[len];
+  const double count = max(1, live);
+  if (set == 0 && c < len) {
+    p.counts[e] = n;
+    if (p.mean_p) p.mean_p[e] = (float)(q / count);
+  }
+  if (tid < kCluster) {  // the slice's part of the loss, and its number of pairs
+    double x = 0;
+    int b = 0;
+    for (int i = 0; i < len; ++i) x += s.sum[i] * s.slice[i], b += s.slice[i];
+    cluster.map_shared_rank(s.loss, tid)[rank] = x;
+    cluster.map_shared_rank(s.base, tid)[rank] = b;
+  }
+  cluster.sync();  // and no CTA leaves before the others have read its parts
+  if (rank == 0 && tid == 0) {
+    p.counts[p.E] = live;
+    double x = 0;
+    for (int i = 0; i < kCluster; ++i) x += s.loss[i];
+    p.loss[0] = (float)(x * p.coef * p.E / (p.k * count * count));
+  }
+  if (p.offsets && tid == 0) {
+    int b = 0;
+    for (int i = 0; i < rank; ++i) b += s.base[i];
+    for (int i = 0; i < len; ++i) {
+      p.offsets[e0 + i] = b;
+      b += s.slice[i];
+    }
+    if (rank == kCluster - 1) p.offsets[p.E] = b;
+  }
+}
+
+// Shared memory: [kWarps][E] sums, then [E] and [E + 1] of the CTA.
+size_t balance_smem(int E) { return ((size_t)kWarps * E + E + E + 1) * 4; }
+
+// Few tokens: one cluster does it all.
+template <class Tok> __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) balance_one_kernel(const BalanceParams p) {
+  extern __shared__ double smem[];
+  Finish &s = *reinterpret_cast<Finish *>(smem);
+  float *s_w = reinterpret_cast<float *>(&s + 1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cg::cluster_group cluster = cg::this_cluster();
+  float *s_p = s_w + kWarps * p.E;
+  int32_t *s_c = reinterpret_cast<int32_t *>(s_p + p.E);
+  count_tokens<Tok>(p, (int)cluster.block_rank(), kCluster, s_w, s_p, s_c);
+  cluster.sync();
+  finish(
+      p, s, kCluster, [&](int g, int e) { return cluster.map_shared_rank(s_p, g)[e]; },
+      [&](int g, int e) { return cluster.map_shared_rank(s_c, g)[e]; });
+}
+
+template <class Tok> __global__ void __launch_bounds__(kThreads, 2) balance_part_kernel(const BalanceParams p) {
+  extern __shared__ double smem[];
+  float *s_w = reinterpret_cast<float *>(smem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float *s_p = s_w + kWarps * p.E;
+  int32_t *s_c = reinterpret_cast<int32_t *>(s_p + p.E);
+  count_tokens<Tok>(p, blockIdx.x, gridDim.x, s_w, s_p, s_c);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kThreads) p.part_p[(size_t)blockIdx.x * p.E + e] = s_p[e];
   for (int e = threadIdx.x; e <= p.E; e += kThreads) p.part_c[(size_t)blockIdx.x * (p.E + 1) + e] = s_c[e];
 }
 
-__global__ void __launch_bounds__(kThreads) balance_finish_kernel(const BalanceParams p, int ctas) { finish(p, ctas); }
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) balance_finish_kernel(const BalanceParams p) {
+  extern __shared__ double smem[];
+  Finish &s = *reinterpret_cast<Finish *>(smem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  finish(
+      p, s, p.parts, [&](int g, int e) { return p.part_p[(size_t)g * p.E + e]; },
+      [&](int g, int e) { return p.part_c[(size_t)g * (p.E + 1) + e]; });
+}
 
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const float *logits, const int32_t *counts,
-                                                                const uint8_t *mask, int T, int E, int k, float coef,
-                                                                const float *dloss, float *dlogits) {
-  extern __shared__ float s_f[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  long long total = 0;
-  for (int e = 0; e < E; ++e) total += counts[e];
+// f_e less its mean: a softmax's gradient does not see a constant, and a
+// difference of two nearly equal sums would lose what f's differences hold.
+// dlogits may be logits: a token's lanes have read it before they write it.
+constexpr int kGradThreads = 128;
+
+template <class Tok> __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const float *logits, const int32_t *counts, const uint8_t *mask,
+                                                                                         int T, int E, int k, float coef,
+                                                                                         const float *dloss, float *dlogits) {
+  __shared__ int32_t s_total[kGradThreads / 32];
+  const int tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kRows = Tok::kTokens * (kGradThreads / 32);
+  float z[Tok::kNV];
+  auto fetch = [&](int t) {
+    const bool live = t < T && (!mask || mask[t] != 0);
+#pragma unroll
+    for (int j = 0; j < Tok::kNV; ++j) z[j] = -INFINITY;
+    if (live) Tok::load(z, logits + (size_t)t * E, E);
+  };
+  int t = blockIdx.x * kRows + tid / (32 / Tok::kTokens);
+  fetch(t);
+  int total = 0;
+  for (int e = tid; e < E; e += kGradThreads) total += counts[e];
+  total = __reduce_add_sync(0xffffffffu, total);
+  if ((tid & 31) == 0) s_total[tid >> 5] = total;
   const double n = max(1, counts[E]);
-  for (int e = tid; e < E; e += kThreads) s_f[e] = (float)(((double)counts[e] - (double)total / E) / (k * n));
-  __syncthreads();
   const float scale = (float)((dloss ? (double)dloss[0] : 1.0) * coef * E / n);
-  for (int t = blockIdx.x * kWarps + warp; t < T; t += gridDim.x * kWarps) {
-    const float *z = logits + (size_t)t * E;
-    float *d = dlogits + (size_t)t * E;
-    float m = -INFINITY, sum = 0.f, dot = 0.f;
-    bool nan = false;
-    const bool live = !mask || mask[t] != 0;
-    if (live) {
-      for (int e = lane; e < E; e += 32) m = fmaxf(m, z[e]), nan |= z[e] != z[e];
-      m = warp_max(m);
-      if (__any_sync(0xffffffffu, nan)) m = NAN;
-    }
-    if (m == -INFINITY) {
-      for (int e = lane; e < E; e += 32) d[e] = 0.f;
-      continue;
-    }
-    for (int e = lane; e < E; e += 32) {
-      const float x = expf(z[e] - m);
-      sum += x;
-      dot += x * s_f[e];
-    }
-    sum = warp_add(sum);
-    dot = warp_add(dot) / sum;
-    for (int e = lane; e < E; e += 32) d[e] = scale * (expf(z[e] - m) / sum) * (s_f[e] - dot);
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kGradThreads / 32; ++w) total += s_total[w];
+  const double mean = (double)total / E, share = 1. / (k * n);
+  float f[Tok::kNV];
+#pragma unroll
+  for (int j = 0; j < Tok::kNV; ++j) f[j] = Tok::column(j) < E ? (float)((counts[Tok::column(j)] - mean) * share) : 0.f;
+  for (;;) {
+    Tok::exps(z);
+    float d = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < Tok::kNV; ++j) d += z[j], dot = fmaf(z[j], f[j], dot);
+    d = Tok::sum(d);
+    dot = Tok::sum(dot);
+    const float r = d == 0.f ? 0.f : 1.f / d;
+    dot *= r;
+    const float by = d == 0.f ? 0.f : scale * r;
+#pragma unroll
+    for (int j = 0; j < Tok::kNV; ++j) z[j] = by * z[j] * (f[j] - dot);
+    if (t < T) Tok::store(dlogits + (size_t)t * E, z, E);
+    t += gridDim.x * kRows;
+    if (t - tid / (32 / Tok::kTokens) >= T) break;
+    fetch(t);
   }
+}
+
+// The kernels for E: lanes of a token, logits of a lane.
+template <class F> int32_t with_token(int E, F f) {
+  auto pick = [&](auto vec) {
+    constexpr bool V = decltype(vec)::value;
+    if (E <= 32) return f(Token<8, 4, V>{});
+    if (E <= 64) return f(Token<8, 8, V>{});
+    if (E <= 128) return f(Token<8, 16, V>{});
+    if (E <= 256) return f(Token<16, 16, V>{});
+    if (E <= 512) return f(Token<32, 16, V>{});
+    return f(Token<32, 32, V>{});
+  };
+  return E % 4 == 0 ? pick(std::true_type{}) : pick(std::false_type{});
+}
+
+template <class K, class... Args> int32_t launch(K k, int ctas, int threads, size_t smem, cudaStream_t s, Args... args) {
+  if (int32_t st = ensure_smem((const void *)k, smem)) return st;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (int32_t st = cuda_status(cudaLaunchKernelEx(&cfg, k, args...))) return st;
+  return launch_status();
 }
 
 int32_t check_sizes(int32_t T, int32_t E, int32_t k) {
@@ -189,23 +357,23 @@ extern "C" int32_t nslm_moe_balance(const float *logits, const int32_t *ids, con
   if (need && (!ws || ws_bytes < need)) return NSLM_ERR_WORKSPACE;
   if (need && !aligned16(ws)) return NSLM_ERR_ALIGN;
   if ((st = check_device())) return st;
-  BalanceParams p{logits, ids, mask, T, E, k, coef, counts, offsets, mean_p, loss, nullptr, nullptr};
+  BalanceParams p{logits, ids, mask, T, E, k, coef, counts, offsets, mean_p, loss, nullptr, nullptr, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const size_t smem = ((size_t)kWarps * E + E + 1) * 4;
   if (T <= kOneLaunchT) {
-    if ((st = ensure_smem((const void *)balance_one_kernel, smem))) return st;
-    balance_one_kernel<<<1, kThreads, smem, s>>>(p);
-    st = launch_status();
+    st = with_token(E, [&](auto tok) {
+      return launch(balance_one_kernel<decltype(tok)>, kCluster, kThreads, sizeof(Finish) + balance_smem(E), s, p);
+    });
     if (st == NSLM_OK) g_launches = 1;
     return st;
   }
   p.part_p = reinterpret_cast<float *>(ws);
   p.part_c = reinterpret_cast<int32_t *>(p.part_p + (size_t)kMaxCtas * E);
-  if ((st = ensure_smem((const void *)balance_part_kernel, smem))) return st;
-  const int ctas = std::max(1, std::min((T + kWarps - 1) / kWarps, kMaxCtas));
-  balance_part_kernel<<<ctas, kThreads, smem, s>>>(p);
-  balance_finish_kernel<<<1, kThreads, 0, s>>>(p, ctas);
-  st = launch_status();
+  st = with_token(E, [&](auto tok) {
+    using Tok = decltype(tok);
+    p.parts = std::min({ceil_div(T, Tok::kTokens * kWarps), 2 * num_sms(), kMaxCtas});
+    return launch(balance_part_kernel<Tok>, p.parts, kThreads, balance_smem(E), s, p);
+  });
+  if (st == NSLM_OK) st = launch(balance_finish_kernel, kCluster, kThreads, sizeof(Finish), s, p);
   if (st == NSLM_OK) g_launches = 2;
   return st;
 }
@@ -221,10 +389,12 @@ extern "C" int32_t nslm_moe_balance_grad(const float *logits, const int32_t *cou
     return NSLM_ERR_ALIGN;
   if ((st = check_device())) return st;
   if (T == 0) return NSLM_OK;
-  const int ctas = std::min((T + kWarps - 1) / kWarps, 8 * num_sms());
-  balance_grad_kernel<<<ctas, kThreads, E * 4, reinterpret_cast<cudaStream_t>(stream)>>>(logits, counts, mask, T, E, k,
-                                                                                        coef, dloss, dlogits);
-  st = launch_status();
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = with_token(E, [&](auto tok) {
+    using Tok = decltype(tok);
+    const int ctas = std::min(ceil_div(T, Tok::kTokens * (kGradThreads / 32)), 12 * num_sms());
+    return launch(balance_grad_kernel<Tok>, ctas, kGradThreads, 0, s, logits, counts, mask, T, E, k, coef, dloss, dlogits);
+  });
   if (st == NSLM_OK) g_launches = 1;
   return st;
 }
