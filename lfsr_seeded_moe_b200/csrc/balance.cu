@@ -13,10 +13,11 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxE = 1024;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 512;
 constexpr int kCluster = 8;
 constexpr int kOneLaunchT = 1024;  // up to here one cluster does it all, and there is no workspace
-constexpr int kMaxCtas = 296;      // CTAs that leave parts in the workspace
+constexpr int kPartThreads = 768;  // leaves the CTAs of the end their registers, so that they wait on their SMs
+constexpr int kMaxCtas = 148;      // CTAs that leave parts in the workspace
 
 struct BalanceParams {
   const float *logits;
@@ -30,6 +31,13 @@ struct BalanceParams {
   int32_t *part_c;  // [CTAs][E + 1]
   int32_t parts;
 };
+
+// 2 steps off at most; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // LANES neighbouring lanes have a token, NV of its logits each: fours of
 // neighbours where E is a multiple of 4 (VEC), else every LANES-th.  A token's
@@ -82,36 +90,58 @@ template <int LANES, int NV, bool VEC> struct Token {
     for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float from = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) z[j] = expf(z[j] - from);
+    for (int j = 0; j < NV; ++j) z[j] = exp2_fast((z[j] - from) * 1.44269504089f);
   }
 };
 
 // The CTA's tokens of a grid of `ctas`: the probabilities' sums to s_p[E], the
-// counts and the number of tokens to s_c[E + 1].  s_w: kWarps x E.
-template <class Tok> __device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, int ctas, float *s_w, float *s_p, int32_t *s_c) {
+// counts and the number of tokens to s_c[E + 1].  s_w: a row of E for each warp.
+template <class Tok, int THREADS>
+__device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, int ctas, float *s_w, float *s_p, int32_t *s_c) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i <= p.E; i += kThreads) s_c[i] = 0;
-  __syncthreads();
-  int n = 0;
-  for (int t = cta * kThreads + tid; t < p.T; t += ctas * kThreads) {
-    if (p.mask && p.mask[t] == 0) continue;
-    ++n;
-    for (int q = 0; q < p.k; ++q) {
-      const int e = p.ids[(size_t)t * p.k + q];
-      if (e >= 0 && e < p.E) atomicAdd(&s_c[e], 1);
-    }
-  }
-  n = __reduce_add_sync(0xffffffffu, n);
-  if (lane == 0) atomicAdd(&s_c[p.E], n);
-  float acc[Tok::kNV] = {};
-  constexpr int kRows = Tok::kTokens * kWarps;
-  for (int t0 = cta * kRows; t0 < p.T; t0 += ctas * kRows) {
-    const int t = t0 + tid / (32 / Tok::kTokens);
+  constexpr int kWarps = THREADS / 32, kRows = Tok::kTokens * kWarps;
+  float z[Tok::kNV];
+  auto fetch = [&](int t) {
     const bool live = t < p.T && (!p.mask || p.mask[t] != 0);
-    float z[Tok::kNV];
 #pragma unroll
     for (int j = 0; j < Tok::kNV; ++j) z[j] = -INFINITY;
     if (live) Tok::load(z, p.logits + (size_t)t * p.E, p.E);
+  };
+  // the first token's pairs and logits, on their way while the counts are cleared
+  int ids[8];
+  bool live = false;
+  auto pairs = [&](int t) {
+    live = t < p.T && (!p.mask || p.mask[t] != 0);
+    if (p.k % 4 == 0) {
+#pragma unroll
+      for (int q = 0; q < 8; q += 4) {
+        int4 v = make_int4(-1, -1, -1, -1);
+        if (live && q < p.k) v = *reinterpret_cast<const int4 *>(p.ids + (size_t)t * p.k + q);
+        ids[q] = v.x, ids[q + 1] = v.y, ids[q + 2] = v.z, ids[q + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) ids[q] = live && q < p.k ? p.ids[(size_t)t * p.k + q] : -1;
+    }
+  };
+  pairs(cta * THREADS + tid);
+  const int mine = tid / (32 / Tok::kTokens);
+  fetch(cta * kRows + mine);
+  for (int i = tid; i <= p.E; i += THREADS) s_c[i] = 0;
+  __syncthreads();
+  int n = 0;
+  for (int t = cta * THREADS + tid; t < p.T;) {
+    n += live;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (ids[q] >= 0 && ids[q] < p.E) atomicAdd(&s_c[ids[q]], 1);
+    t += ctas * THREADS;
+    if (t < p.T) pairs(t);
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0 && n) atomicAdd(&s_c[p.E], n);
+  float acc[Tok::kNV] = {};
+  for (int t0 = cta * kRows; t0 < p.T;) {
     Tok::exps(z);
     float d = 0.f;
 #pragma unroll
@@ -120,15 +150,28 @@ template <class Tok> __device__ __forceinline__ void count_tokens(const BalanceP
     const float r = d == 0.f ? 0.f : 1.f / d;  // nothing left in the row: nothing to add
 #pragma unroll
     for (int j = 0; j < Tok::kNV; ++j) acc[j] = fmaf(z[j], r, acc[j]);
+    t0 += ctas * kRows;
+    if (t0 < p.T) fetch(t0 + mine);
+  }
+  // over the warp's tokens: each halving leaves a lane half of the columns
+  int keep = Tok::kNV, from = 0;
+#pragma unroll
+  for (int o = 16; o >= 32 / Tok::kTokens; o >>= 1) {
+    keep /= 2;
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < Tok::kNV / 2; ++j) {
+      if (j >= keep) break;
+      const float other = __shfl_xor_sync(0xffffffffu, up ? acc[j] : acc[j + keep], o);
+      acc[j] = (up ? acc[j + keep] : acc[j]) + other;
+    }
+    from += up ? keep : 0;
   }
 #pragma unroll
-  for (int j = 0; j < Tok::kNV; ++j) {
-#pragma unroll
-    for (int o = 32 / Tok::kTokens; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-    if (lane < 32 / Tok::kTokens && Tok::column(j) < p.E) s_w[warp * p.E + Tok::column(j)] = acc[j];
-  }
+  for (int j = 0; j < Tok::kNV / Tok::kTokens; ++j)
+    if (Tok::column(from + j) < p.E) s_w[warp * p.E + Tok::column(from + j)] = acc[j];
   __syncthreads();
-  for (int e = tid; e < p.E; e += kThreads) {
+  for (int e = tid; e < p.E; e += THREADS) {
     float q = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) q += s_w[w * p.E + e];
@@ -136,10 +179,16 @@ template <class Tok> __device__ __forceinline__ void count_tokens(const BalanceP
   }
 }
 
+__device__ __forceinline__ void sync_cluster(int ctas) {
+  if (ctas == 1) __syncthreads();
+  else cg::this_cluster().sync();
+}
+
 struct Finish {
   double sum[kThreads];
   int32_t count[kThreads];
-  int32_t slice[kMaxE / kCluster + 1];
+  double total[kMaxE + 1];
+  int32_t slice[kMaxE + 1];
   double loss[kCluster];
   int32_t base[kCluster];
 };
@@ -148,25 +197,28 @@ struct Finish {
 // and tokens(g, e) give the sums and counts of g's tokens, e = E their number.
 template <class P, class C> __device__ void finish(const BalanceParams &p, Finish &s, int parts, P part, C tokens) {
   cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
-  const int e0 = p.E * rank / kCluster, len = p.E * (rank + 1) / kCluster - e0;
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int e0 = p.E * rank / ctas, len = p.E * (rank + 1) / ctas - e0;
   // a column for each expert of the slice, and one for the number of tokens
-  const int cols = len + 1, sets = kThreads / cols, set = tid / cols, c = tid - set * cols;
+  const int cols = len + 1, sets = min(kThreads / cols, parts), set = tid / cols, c = tid - set * cols;
   const int e = c < len ? e0 + c : p.E;
   double q = 0;
   int n = 0;
-  if (set < sets)
+  if (set < sets) {
+#pragma unroll 8
     for (int g = set; g < parts; g += sets) {
-      if (c < len) q += part(g, e);
+      q += c < len ? part(g, e) : 0.f;
       n += tokens(g, e);
     }
-  s.sum[tid] = q;
-  s.count[tid] = n;
+    s.sum[tid] = q;
+    s.count[tid] = n;
+  }
   __syncthreads();
   if (set == 0) {
+#pragma unroll 4
     for (int i = 1; i < sets; ++i) q += s.sum[i * cols + c], n += s.count[i * cols + c];
     s.slice[c] = n;
-    s.sum[c] = q;
+    s.total[c] = q;
   }
   __syncthreads();
   const int live = s.slice[len];
@@ -175,65 +227,78 @@ template <class P, class C> __device__ void finish(const BalanceParams &p, Finis
     p.counts[e] = n;
     if (p.mean_p) p.mean_p[e] = (float)(q / count);
   }
-  if (tid < kCluster) {  // the slice's part of the loss, and its number of pairs
+  if (tid < 32) {  // the slice's part of the loss, and its number of pairs
     double x = 0;
     int b = 0;
-    for (int i = 0; i < len; ++i) x += s.sum[i] * s.slice[i], b += s.slice[i];
-    cluster.map_shared_rank(s.loss, tid)[rank] = x;
-    cluster.map_shared_rank(s.base, tid)[rank] = b;
+    for (int i = tid; i < len; i += 32) x += s.total[i] * s.slice[i], b += s.slice[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    b = __reduce_add_sync(0xffffffffu, b);
+    if (tid < ctas) {
+      cluster.map_shared_rank(s.loss, tid)[rank] = x;
+      cluster.map_shared_rank(s.base, tid)[rank] = b;
+    }
   }
-  cluster.sync();  // and no CTA leaves before the others have read its parts
-  if (rank == 0 && tid == 0) {
+  sync_cluster(ctas);  // and no CTA leaves before the others have read its parts
+  if (rank == 0 && tid == 32) {
     p.counts[p.E] = live;
     double x = 0;
-    for (int i = 0; i < kCluster; ++i) x += s.loss[i];
+    for (int i = 0; i < ctas; ++i) x += s.loss[i];
     p.loss[0] = (float)(x * p.coef * p.E / (p.k * count * count));
   }
-  if (p.offsets && tid == 0) {
+  if (p.offsets && tid < 32) {
     int b = 0;
     for (int i = 0; i < rank; ++i) b += s.base[i];
-    for (int i = 0; i < len; ++i) {
-      p.offsets[e0 + i] = b;
-      b += s.slice[i];
+    for (int i0 = 0; i0 < len; i0 += 32) {
+      const int own = i0 + tid < len ? s.slice[i0 + tid] : 0;
+      int upto = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (tid >= o) upto += y;
+      }
+      if (i0 + tid < len) p.offsets[e0 + i0 + tid] = b + upto - own;
+      b += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (rank == kCluster - 1) p.offsets[p.E] = b;
+    if (rank == ctas - 1 && tid == 0) p.offsets[p.E] = b;
   }
 }
 
-// Shared memory: [kWarps][E] sums, then [E] and [E + 1] of the CTA.
-size_t balance_smem(int E) { return ((size_t)kWarps * E + E + E + 1) * 4; }
+// Shared memory: a row of E sums for each warp, then [E] and [E + 1] of the CTA.
+size_t balance_smem(int E, int threads) { return ((size_t)threads / 32 * E + E + E + 1) * 4; }
 
 // Few tokens: one cluster does it all.
-template <class Tok> __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) balance_one_kernel(const BalanceParams p) {
+template <class Tok> __global__ void __launch_bounds__(kThreads) balance_one_kernel(const BalanceParams p) {
   extern __shared__ double smem[];
   Finish &s = *reinterpret_cast<Finish *>(smem);
   float *s_w = reinterpret_cast<float *>(&s + 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
-  float *s_p = s_w + kWarps * p.E;
+  float *s_p = s_w + kThreads / 32 * p.E;
   int32_t *s_c = reinterpret_cast<int32_t *>(s_p + p.E);
-  count_tokens<Tok>(p, (int)cluster.block_rank(), kCluster, s_w, s_p, s_c);
-  cluster.sync();
+  const int ctas = (int)cluster.num_blocks();
+  count_tokens<Tok, kThreads>(p, (int)cluster.block_rank(), ctas, s_w, s_p, s_c);
+  sync_cluster(ctas);
   finish(
-      p, s, kCluster, [&](int g, int e) { return cluster.map_shared_rank(s_p, g)[e]; },
+      p, s, ctas, [&](int g, int e) { return cluster.map_shared_rank(s_p, g)[e]; },
       [&](int g, int e) { return cluster.map_shared_rank(s_c, g)[e]; });
 }
 
-template <class Tok> __global__ void __launch_bounds__(kThreads, 2) balance_part_kernel(const BalanceParams p) {
+template <class Tok> __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(const BalanceParams p) {
   extern __shared__ double smem[];
   float *s_w = reinterpret_cast<float *>(smem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  float *s_p = s_w + kWarps * p.E;
+  float *s_p = s_w + kPartThreads / 32 * p.E;
   int32_t *s_c = reinterpret_cast<int32_t *>(s_p + p.E);
-  count_tokens<Tok>(p, blockIdx.x, gridDim.x, s_w, s_p, s_c);
+  count_tokens<Tok, kPartThreads>(p, blockIdx.x, gridDim.x, s_w, s_p, s_c);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kThreads) p.part_p[(size_t)blockIdx.x * p.E + e] = s_p[e];
-  for (int e = threadIdx.x; e <= p.E; e += kThreads) p.part_c[(size_t)blockIdx.x * (p.E + 1) + e] = s_c[e];
+  for (int e = threadIdx.x; e < p.E; e += kPartThreads) p.part_p[(size_t)blockIdx.x * p.E + e] = s_p[e];
+  for (int e = threadIdx.x; e <= p.E; e += kPartThreads) p.part_c[(size_t)blockIdx.x * (p.E + 1) + e] = s_c[e];
 }
 
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) balance_finish_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(kThreads) balance_finish_kernel(const BalanceParams p) {
   extern __shared__ double smem[];
   Finish &s = *reinterpret_cast<Finish *>(smem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -312,18 +377,22 @@ template <class F> int32_t with_token(int E, F f) {
   return E % 4 == 0 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
-template <class K, class... Args> int32_t launch(K k, int ctas, int threads, size_t smem, cudaStream_t s, Args... args) {
+template <class K, class... Args>
+int32_t launch(K k, int ctas, int cluster, int threads, size_t smem, cudaStream_t s, Args... args) {
   if (int32_t st = ensure_smem((const void *)k, smem)) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (int32_t st = cuda_status(cudaLaunchKernelEx(&cfg, k, args...))) return st;
   return launch_status();
 }
@@ -360,8 +429,11 @@ extern "C" int32_t nslm_moe_balance(const float *logits, const int32_t *ids, con
   BalanceParams p{logits, ids, mask, T, E, k, coef, counts, offsets, mean_p, loss, nullptr, nullptr, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T <= kOneLaunchT) {
+    // a cluster's barriers cost about what 64 tokens do, and a CTA has a thread for each column of its slice and one more in the end
+    int ctas = 1;
+    while (ctas < kCluster && (T > 64 * ctas || ceil_div(E, ctas) + 1 > kThreads)) ctas *= 2;
     st = with_token(E, [&](auto tok) {
-      return launch(balance_one_kernel<decltype(tok)>, kCluster, kThreads, sizeof(Finish) + balance_smem(E), s, p);
+      return launch(balance_one_kernel<decltype(tok)>, ctas, ctas, kThreads, sizeof(Finish) + balance_smem(E, kThreads), s, p);
     });
     if (st == NSLM_OK) g_launches = 1;
     return st;
@@ -370,10 +442,10 @@ extern "C" int32_t nslm_moe_balance(const float *logits, const int32_t *ids, con
   p.part_c = reinterpret_cast<int32_t *>(p.part_p + (size_t)kMaxCtas * E);
   st = with_token(E, [&](auto tok) {
     using Tok = decltype(tok);
-    p.parts = std::min({ceil_div(T, Tok::kTokens * kWarps), 2 * num_sms(), kMaxCtas});
-    return launch(balance_part_kernel<Tok>, p.parts, kThreads, balance_smem(E), s, p);
+    p.parts = std::min({ceil_div(T, Tok::kTokens * kPartThreads / 32), num_sms(), kMaxCtas});
+    return launch(balance_part_kernel<Tok>, p.parts, 1, kPartThreads, balance_smem(E, kPartThreads), s, p);
   });
-  if (st == NSLM_OK) st = launch(balance_finish_kernel, kCluster, kThreads, sizeof(Finish), s, p);
+  if (st == NSLM_OK) st = launch(balance_finish_kernel, kCluster, kCluster, kThreads, sizeof(Finish), s, p);
   if (st == NSLM_OK) g_launches = 2;
   return st;
 }
@@ -393,7 +465,7 @@ extern "C" int32_t nslm_moe_balance_grad(const float *logits, const int32_t *cou
   st = with_token(E, [&](auto tok) {
     using Tok = decltype(tok);
     const int ctas = std::min(ceil_div(T, Tok::kTokens * (kGradThreads / 32)), 12 * num_sms());
-    return launch(balance_grad_kernel<Tok>, ctas, kGradThreads, 0, s, logits, counts, mask, T, E, k, coef, dloss, dlogits);
+    return launch(balance_grad_kernel<Tok>, ctas, 1, kGradThreads, 0, s, logits, counts, mask, T, E, k, coef, dloss, dlogits);
   });
   if (st == NSLM_OK) g_launches = 1;
   return st;
