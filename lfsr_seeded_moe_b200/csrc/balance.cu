@@ -205,27 +205,35 @@ template <class P, class C> __device__ void finish(const BalanceParams &p, Finis
   double q = 0;
   int n = 0;
   if (set < sets) {
-#pragma unroll 8
-    for (int g = set; g < parts; g += sets) {
-      q += c < len ? part(g, e) : 0.f;
-      n += tokens(g, e);
+    // eight parts' loads in flight
+    for (int g = set; g < parts; g += 8 * sets) {
+      float x[8];
+      int y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool there = g + i * sets < parts;
+        x[i] = there && c < len ? part(g + i * sets, e) : 0.f;
+        y[i] = there ? tokens(g + i * sets, e) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q += x[i], n += y[i];
     }
     s.sum[tid] = q;
     s.count[tid] = n;
   }
   __syncthreads();
   if (set == 0) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 1; i < sets; ++i) q += s.sum[i * cols + c], n += s.count[i * cols + c];
     s.slice[c] = n;
     s.total[c] = q;
   }
   __syncthreads();
   const int live = s.slice[len];
-  const double count = max(1, live);
+  const double share = 1. / max(1, live);
   if (set == 0 && c < len) {
     p.counts[e] = n;
-    if (p.mean_p) p.mean_p[e] = (float)(q / count);
+    if (p.mean_p) p.mean_p[e] = (float)(q * share);
   }
   if (tid < 32) {  // the slice's part of the loss, and its number of pairs
     double x = 0;
@@ -239,12 +247,13 @@ template <class P, class C> __device__ void finish(const BalanceParams &p, Finis
       cluster.map_shared_rank(s.base, tid)[rank] = b;
     }
   }
+  const double scale = share * share * p.coef * p.E / p.k;
   sync_cluster(ctas);  // and no CTA leaves before the others have read its parts
   if (rank == 0 && tid == 32) {
     p.counts[p.E] = live;
     double x = 0;
     for (int i = 0; i < ctas; ++i) x += s.loss[i];
-    p.loss[0] = (float)(x * p.coef * p.E / (p.k * count * count));
+    p.loss[0] = (float)(x * scale);
   }
   if (p.offsets && tid < 32) {
     int b = 0;
