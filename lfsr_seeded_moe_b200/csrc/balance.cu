@@ -330,12 +330,12 @@ template <class Tok> __global__ void __launch_bounds__(kGradThreads) balance_gra
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kRows = Tok::kTokens * (kGradThreads / 32);
-  float z[Tok::kNV];
+  float z[Tok::kNV], ahead[Tok::kNV];  // a token's logits, and the next one's on their way
   auto fetch = [&](int t) {
     const bool live = t < T && (!mask || mask[t] != 0);
 #pragma unroll
-    for (int j = 0; j < Tok::kNV; ++j) z[j] = -INFINITY;
-    if (live) Tok::load(z, logits + (size_t)t * E, E);
+    for (int j = 0; j < Tok::kNV; ++j) ahead[j] = -INFINITY;
+    if (live) Tok::load(ahead, logits + (size_t)t * E, E);
   };
   int t = blockIdx.x * kRows + tid / (32 / Tok::kTokens);
   fetch(t);
@@ -353,7 +353,10 @@ template <class Tok> __global__ void __launch_bounds__(kGradThreads) balance_gra
   float f[Tok::kNV];
 #pragma unroll
   for (int j = 0; j < Tok::kNV; ++j) f[j] = Tok::column(j) < E ? (float)((counts[Tok::column(j)] - mean) * share) : 0.f;
-  for (;;) {
+  for (; t - tid / (32 / Tok::kTokens) < T; t += gridDim.x * kRows) {
+#pragma unroll
+    for (int j = 0; j < Tok::kNV; ++j) z[j] = ahead[j];
+    fetch(t + gridDim.x * kRows);
     Tok::exps(z);
     float d = 0.f, dot = 0.f;
 #pragma unroll
@@ -366,9 +369,6 @@ template <class Tok> __global__ void __launch_bounds__(kGradThreads) balance_gra
 #pragma unroll
     for (int j = 0; j < Tok::kNV; ++j) z[j] = by * z[j] * (f[j] - dot);
     if (t < T) Tok::store(dlogits + (size_t)t * E, z, E);
-    t += gridDim.x * kRows;
-    if (t - tid / (32 / Tok::kTokens) >= T) break;
-    fetch(t);
   }
 }
 
@@ -473,8 +473,12 @@ extern "C" int32_t nslm_moe_balance_grad(const float *logits, const int32_t *cou
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = with_token(E, [&](auto tok) {
     using Tok = decltype(tok);
-    const int ctas = std::min(ceil_div(T, Tok::kTokens * (kGradThreads / 32)), 12 * num_sms());
-    return launch(balance_grad_kernel<Tok>, ctas, 1, kGradThreads, 0, s, logits, counts, mask, T, E, k, coef, dloss, dlogits);
+    auto k_grad = balance_grad_kernel<Tok>;
+    // one wave, and CTAs with equal numbers of rounds
+    const int rounds = ceil_div(T, Tok::kTokens * (kGradThreads / 32));
+    const int most = max_active_ctas((const void *)k_grad, kGradThreads, 0) * num_sms();
+    const int ctas = ceil_div(rounds, ceil_div(rounds, most));
+    return launch(k_grad, ctas, 1, kGradThreads, 0, s, logits, counts, mask, T, E, k, coef, dloss, dlogits);
   });
   if (st == NSLM_OK) g_launches = 1;
   return st;
