@@ -299,21 +299,22 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
       }
       xp += x_stage;
     }
-    float *rb = red + buf * WARPS * kMaxVec * kTile;
-    float *rw = rb + warp * kMaxVec * kTile + g;
+    // sums over the tile's warps; only these wait for one another
+    float *rb = red + (buf * WARPS + sub * p.kw) * kMaxVec * kTile;
+    float *rw = rb + kp * kMaxVec * kTile + g;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int m = 2 * t + (r & 1);
       if (m < MP) rw[m * kTile + 8 * (r >> 1)] = acc[r] + (AFFINE ? fmaf(8.f, c_sc[r], c_of[r]) : 0.f);
     }
-    __syncthreads();
-    for (int i = tid; i < tps * kMaxVec * kTile; i += WARPS * 32) {
-      const int tile = i / (kMaxVec * kTile), m = i / kTile % kMaxVec;
-      const int row = (step * tps + tile) * kTile + i % kTile;
+    if (p.kw == 1) __syncwarp();
+    else if (p.kw == WARPS) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(p.kw * 32) : "memory");
+    for (int i = kp * 32 + lane; i < MP * kTile; i += p.kw * 32) {
+      const int m = i / kTile, row = (step * tps + sub) * kTile + i % kTile;
       if (m >= M || row >= N) continue;
-      const float *at = rb + tile * (p.kw - 1) * kMaxVec * kTile + i;
       float s = 0.f;
-      for (int k = 0; k < p.kw; ++k) s += at[k * kMaxVec * kTile];
+      for (int k = 0; k < p.kw; ++k) s += rb[k * kMaxVec * kTile + i];
       p.y[(size_t)m * N + row] = s;
     }
   }
