@@ -14,11 +14,13 @@ constexpr int kMaxMK = 65536;  // bf16 activations of one call that stay in shar
 
 __device__ __forceinline__ float bf16_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
-// A tile is 16 rows.  kw warps of a CTA share a tile, each with a range of the
-// groups along K, and add their sums in shared memory at its end; a CTA has
-// WARPS / kw tiles at a time and walks over the rows.  Weights come by cp.async
-// into a ring of STAGES x (16 rows x 256 weights) of each warp's own, which
-// runs ahead across tiles, so no load waits for the sums or the barrier.
+// A tile is 16 rows, a stage 256 weights of each, with their scales and offsets.
+// kw warps of a CTA share a tile, each with a range of its stages, and add their
+// sums in shared memory at its end; a CTA has WARPS / kw tiles at a time and
+// walks over the rows.  Stages come by cp.async into a ring of each warp's own,
+// which runs ahead across tiles, so no load waits for the sums or the barrier.
+// (Loads into registers would: those in flight share a few counters with the
+// shared-memory loads of the products, which then wait for them.)
 //
 // The product runs on mma.sync m16n8k16 with the weights as A (q - 8, exact in
 // bf16, straight from the packed words to the fragment's registers) and the
@@ -30,8 +32,8 @@ __device__ __forceinline__ float bf16_f32(uint32_t h) { return __uint_as_float(h
 // the same order.  Each group gets an accumulator of its own, multiplied by the
 // scale in fp32; products are exact, so nothing of a weight is rounded.  The
 // rest of an affine weight, (b + 8 s) times the group's sum of x, is a product
-// over the groups with b and s as they are stored (bf16) and the sum in three
-// bf16 parts (24 bits), 6 mma for every 16 groups.
+// over the groups, [b s] times [x's sum, 8 times that], with b and s as they are
+// stored (bf16) and the sums in three bf16 parts (24 bits): 3 mma a stage.
 
 constexpr int kTile = 16;
 constexpr int kStageK = 256;             // weights of a row in a stage
@@ -43,10 +45,10 @@ struct Q4Params {
   nslm_q4_matrix W;
   const uint16_t *x;
   float *y;
-  int32_t M, NG;    // NG: groups of a row
+  int32_t M, NG, NS;  // NG, NS: groups and stages of a row
   int32_t kw;       // warps that share a tile
   int32_t steps;    // tiles / (WARPS / kw), rounded up
-  int32_t pos;      // group positions of a vector's sums: 16 ceil(most groups of a warp / 16) for each of kw
+  int32_t spc;      // stages whose scales are copied at once
   bool ready;
 };
 
@@ -55,6 +57,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16_k8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0));
 }
 
 // The bf16 pair (w_i - 8, w_{i+4} - 8) of a word: 0x4300 | q is 128 + q.
@@ -72,9 +80,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
 template <int WORDS>
@@ -89,46 +97,73 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// 4, 8 or 16 bytes.
+template <int BYTES> __device__ __forceinline__ void copy(uint32_t dst, const void *src) {
+  if constexpr (BYTES == 16) copy16(dst, src);
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+template <int G> constexpr int kGroups = kStageK / G;             // of a stage: 8, 4 or 2
+// Scales are copied 8 groups (16 bytes) of a row at once where whole rows and
+// the warps' ranges allow it and there are rows enough for it to matter: each
+// row's piece is a transaction of its own, whatever its size.  (8192 weights of
+// 64-weight groups by 8-byte copies: 80 us at 131072 x 4096, by 16-byte ones 66.)
+constexpr int kScaleRow = 16;
+constexpr int kScales = kTile * kScaleRow;
+template <bool AFFINE> constexpr int kSlot = kStage + kScales * (AFFINE ? 2 : 1);
+// A stage's entries of sums of x: [sums, 8 times those] and zeros up to 8 at least.
+template <int G> constexpr int kSums = G == 32 ? 16 : 8;
+
 // MP: vectors in shared memory, M rounded up to 1, 2, 4 or 8 (zeros behind the last).
 template <int G, int MP, int WARPS, int STAGES, bool AFFINE>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel(const Q4Params p) {
   constexpr int kWords = G / 32;       // words of a row and group for each of 4 lanes
-  constexpr int kGps = kStageK / G;    // groups of a stage
-  constexpr int kSpb = 16 / kGps;      // stages of a batch of 16 groups
+  constexpr int kGps = kGroups<G>, kChunk = kScales * (AFFINE ? 2 : 1);
   // The 16-byte chunks of a stage's row change places by the row, so that the
   // rows that one phase of a shared-memory load reads lie in different banks.
   constexpr int kFlip = G / 2;         // in units of a group's bytes
   constexpr int kFlips = kRow / kFlip; // 8, 4 or 2
-  extern __shared__ uint4 smem[];
+  extern __shared__ __align__(128) uint4 smem[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int M = p.M, K = p.W.K, N = p.W.N, NG = p.NG;
+  const int M = p.M, K = p.W.K, N = p.W.N, NG = p.NG, NS = p.NS;
   uint4 *xs = smem + kZero / 16;  // [K / 32][MP][4], behind the zeros
-  uint16_t *sx = reinterpret_cast<uint16_t *>(xs + (size_t)MP * K / 8);  // [3][MP][pos + 8]
-  const int sx_row = p.pos + 8;
-  uint8_t *rings = reinterpret_cast<uint8_t *>(sx) + (AFFINE ? 6 * MP * sx_row : 0);
-  float *red = reinterpret_cast<float *>(rings + WARPS * STAGES * kStage);  // [2][WARPS][8][16]
-  const uint32_t ring = smem_addr(rings) + warp * STAGES * kStage;
+  uint16_t *sx = reinterpret_cast<uint16_t *>(xs + (size_t)MP * K / 8);  // [3][MP][sx_row]
+  const int sx_row = NS * kSums<G> + 8;
+  // on 128 bytes: copies write whole sectors
+  uint8_t *rings = reinterpret_cast<uint8_t *>(sx) + (AFFINE ? (6 * MP * sx_row + 127) & ~127 : 0);
+  float *red = reinterpret_cast<float *>(rings + WARPS * STAGES * kSlot<AFFINE>);  // [2][WARPS][8][16]
+  const uint32_t ring = smem_addr(rings) + warp * STAGES * kSlot<AFFINE>;
 
   const int sub = warp / p.kw, kp = warp - sub * p.kw, tps = WARPS / p.kw;
-  const int g0 = kp * NG / p.kw, g1 = (kp + 1) * NG / p.kw;
-  const int nst = (g1 - g0 + kGps - 1) / kGps;  // stages of a tile
+  // this warp's stages of a tile
+  const int units = (NS + p.spc - 1) / p.spc, st0 = kp * units / p.kw * p.spc;
+  const int nst = min(NS, (kp + 1) * units / p.kw * p.spc) - st0;
+  const bool whole = K % kStageK == 0;  // every stage is, and its scales lie in aligned words
+  const int last = p.spc - 1;           // spc is a power of two
 
-  // the load side: which stage comes next, and its two row pointers
-  int l_step = blockIdx.x, l_st = 0, l_left = 0;
-  uint32_t l_slot = 0;
+  // the load side: which stage comes next, its two row pointers, and the
+  // scales (lanes 0 to 15) or offsets (16 to 31) of one row
+  const int first = sub < tps ? (int)blockIdx.x : p.steps;  // warps that are left over have no tile
+  int l_step = first, l_st = 0, l_left = 0, l_group = 0;
+  uint32_t l_slot = 0, l_chunk = 0;  // the next stage's place, and the next scales'
   const uint8_t *src0 = nullptr, *src1 = nullptr;
+  const uint16_t *src2 = nullptr;
   auto rows_of = [&]() {
-    const int row = (l_step * tps + sub) * kTile + g;
+    const int row = (l_step * tps + sub) * kTile;
     const size_t pitch = (size_t)K / 2;
-    const uint8_t *base = reinterpret_cast<const uint8_t *>(p.W.q) + (size_t)g0 * (G / 2) + t * 16;
-    src0 = base + (size_t)min(row, N - 1) * pitch;
-    src1 = base + (size_t)min(row + 8, N - 1) * pitch;
-    l_left = (g1 - g0) * G - t * 32;
+    const uint8_t *base = reinterpret_cast<const uint8_t *>(p.W.q) + (size_t)st0 * kRow + t * 16;
+    src0 = base + (size_t)min(row + g, N - 1) * pitch;
+    src1 = base + (size_t)min(row + g + 8, N - 1) * pitch;
+    src2 = (AFFINE && lane >= 16 ? p.W.biases : p.W.scales) + (size_t)min(row + lane % 16, N - 1) * NG + st0 * kGps;
+    l_group = st0 * kGps;
+    l_left = K - st0 * kStageK - t * 32;
     l_st = nst;
   };
   // chunks t and t + 4 of rows g and g + 8 are this lane's to copy
   const uint32_t dst0 = ring + g * kRow + ((t * 16) ^ ((g % kFlips) * kFlip));
   const uint32_t dst1 = ring + g * kRow + ((t * 16 + 64) ^ ((g % kFlips) * kFlip));
+  const uint32_t scales = ring + STAGES * kStage;
+  const uint32_t dst2 = scales + (lane / 16) * kScales + (lane % 16) * kScaleRow;
   if (l_step < p.steps) rows_of();
   auto load_stage = [&]() {
     if (l_st > 0) {
@@ -140,7 +175,24 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
         copy16(dst1 + l_slot, src0 + 64);
         copy16(dst1 + l_slot + 8 * kRow, src1 + 64);
       }
-      src0 += kRow, src1 += kRow;
+      if (((nst - l_st) & last) == 0) {
+        if (AFFINE || lane < 16) {
+          if (last) {
+            copy16(dst2 + l_chunk, src2);
+          } else if (whole) {
+            copy<kGps * 2>(dst2 + l_chunk, src2);
+          } else {  // what is behind the row counts as 0
+#pragma unroll
+            for (int j = 0; j < kGps; ++j) {
+              const uint16_t v = l_group + j < NG ? __ldg(src2 + j) : 0;
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst2 + l_chunk + 2 * j), "h"(v) : "memory");
+            }
+          }
+        }
+        l_chunk = l_chunk == (STAGES - 1) * kChunk ? 0 : l_chunk + kChunk;
+      }
+      src0 += kRow, src1 += kRow, src2 += kGps;
+      l_group += kGps;
       l_left -= kStageK;
       l_slot = l_slot == (STAGES - 1) * kStage ? 0 : l_slot + kStage;
       if (--l_st == 0) {
@@ -150,43 +202,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // scales and offsets of 16 groups, one batch ahead: lane t has groups 4t..4t+3
-  // of rows g (words 0, 1) and g + 8 (2, 3), which is the A fragment of a
-  // product over the groups in that order
-  uint32_t sc[4], of[4], sc_next[4], of_next[4];
-  int c_step = blockIdx.x, c_b = 0;
-  const bool quads = ((NG | g0) & 3) == 0;  // four groups' values lie in one aligned word of 8 bytes
-  auto load_scales = [&]() {
-    if (c_step >= p.steps) return;
-    const int row = (c_step * tps + sub) * kTile + g, gi = g0 + c_b * 16 + 4 * t;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const size_t at = (size_t)min(row + 8 * r, N - 1) * NG + gi;
-      uint2 s = make_uint2(0, 0), o = make_uint2(0, 0);
-      if (quads) {
-        if (gi < NG) {  // past the range's end the next warp's, where the sums of x are zero
-          s = __ldg(reinterpret_cast<const uint2 *>(p.W.scales + at));
-          if (AFFINE) o = __ldg(reinterpret_cast<const uint2 *>(p.W.biases + at));
-        }
-      } else {
-        uint32_t v[4] = {}, w[4] = {};
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (gi + h < g1) {
-            v[h] = __ldg(p.W.scales + at + h);
-            if (AFFINE) w[h] = __ldg(p.W.biases + at + h);
-          }
-        s = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-        o = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-      }
-      sc_next[2 * r] = s.x, sc_next[2 * r + 1] = s.y;
-      of_next[2 * r] = o.x, of_next[2 * r + 1] = o.y;
-    }
-    if (++c_b * 16 >= g1 - g0) c_b = 0, c_step += gridDim.x;
-  };
   auto prologue = [&]() {
     for (int i = 0; i < STAGES - 1; ++i) load_stage();
-    load_scales();
   };
 
   if (p.ready) prologue();
@@ -218,12 +235,12 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
 #pragma unroll
       for (int o = 1; o < G / 8; o <<= 1) s += __shfl_xor_sync(mask, s, o);
       if (wi == 0) {
-        const int part = ((gi + 1) * p.kw - 1) / NG;
-        uint16_t *at = sx + m * sx_row + part * (p.pos / p.kw) + gi - part * NG / p.kw;
+        uint16_t *at = sx + m * sx_row + gi / kGps * kSums<G> + gi % kGps;
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
           const __nv_bfloat16 b = __float2bfloat16_rn(s);
           at[j * MP * sx_row] = __bfloat16_as_ushort(b);
+          at[j * MP * sx_row + kGps] = __bfloat16_as_ushort(__float2bfloat16_rn(8.f * __bfloat162float(b)));
           s -= __bfloat162float(b);
         }
       }
@@ -232,45 +249,54 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
   __syncthreads();
 
   // lanes of columns without a vector read the zeros and stay there
-  const uint32_t xb = smem_addr(smem) + (g < MP ? kZero + ((g0 * kWords * MP + g) * 4 + t) * 16 : 0);
+  const uint32_t xb = smem_addr(smem) + (g < MP ? kZero + ((st0 * (kStageK / 32) * MP + g) * 4 + t) * 16 : 0);
   const uint32_t x_stage = g < MP ? kGps * kWords * MP * 64 : 0;
-  const uint32_t sb = smem_addr(sx) + (g < MP ? (g * sx_row + kp * (p.pos / p.kw) + 4 * t) * 2 : 0);
+  const uint32_t sb = smem_addr(sx) + (g < MP ? (g * sx_row + st0 * kSums<G> + 2 * t) * 2 : 0);
+  // where the lane's pair of [b s] of row g stands
+  const uint32_t co = scales + g * kScaleRow +
+                      (kGps == 8 || t < kGps / 2 ? kScales + t * 4 : (t - kGps / 2) * 4);
   const uint32_t a_lane = ring + g * kRow + t * 4 * kWords;
   const uint32_t flip = (g % kFlips) * kFlip;
+  const uint32_t s_lane = scales + g * kScaleRow;
 
-  uint32_t slot = 0;
+  uint32_t slot = 0, chunk = 0;
   int buf = 0;
-  for (int step = blockIdx.x; step < p.steps; step += gridDim.x, buf ^= 1) {
-    float acc[4] = {}, c_of[4] = {}, c_sc[4] = {};
+  for (int step = first; step < p.steps; step += gridDim.x, buf ^= 1) {
+    float acc[4] = {}, c_co[4] = {};
     uint32_t xp = xb;
     for (int st = 0; st < nst; ++st) {
-      const int jb = (st % kSpb) * kGps;  // the stage's first group in its batch
-      if (jb == 0) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sc[r] = sc_next[r], of[r] = of_next[r];
-        load_scales();
-        if (AFFINE) {
-#pragma unroll
-          for (int j = 0; j < 3; ++j) {
-            uint2 b = make_uint2(0, 0);
-            if (g < MP) b = lds64(sb + (j * MP * sx_row + st / kSpb * 16) * 2);
-            mma_bf16(c_of, of[0], of[2], of[1], of[3], b.x, b.y);
-            mma_bf16(c_sc, sc[0], sc[2], sc[1], sc[3], b.x, b.y);
-          }
-        }
-      }
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
       __syncwarp();
       load_stage();
-      const uint32_t rp = a_lane + slot;
-      slot = slot == (STAGES - 1) * kStage ? 0 : slot + kStage;
-      uint32_t s_lo = 0, s_hi = 0;  // two groups' scales of rows g and g + 8
-      auto group = [&](int gi) {
-        if (gi % 2 == 0) {
-          const int from = (lane & ~3) | ((jb | gi) >> 2), word = ((jb | gi) >> 1) & 1;
-          s_lo = __shfl_sync(0xffffffffu, word ? sc[1] : sc[0], from);
-          s_hi = __shfl_sync(0xffffffffu, word ? sc[3] : sc[2], from);
+      const uint32_t rp = a_lane + slot, in = chunk + (st & last) * (kGps * 2), sp = s_lane + in;
+      uint32_t s0w[kGps / 2], s1w[kGps / 2];  // scales of rows g and g + 8
+      lds_words<kGps / 2>(s0w, sp);
+      lds_words<kGps / 2>(s1w, sp + 8 * kScaleRow);
+      if (AFFINE) {
+        const uint32_t at = co + in;
+        uint32_t a0 = 0, a1 = 0;
+        if (t < kGps) a0 = lds32(at), a1 = lds32(at + 8 * kScaleRow);
+        if constexpr (kGps == 8) {
+          const uint32_t a2 = lds32(at - kScales), a3 = lds32(at - kScales + 8 * kScaleRow);
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            const uint32_t from = sb + (j * MP * sx_row + st * kSums<G>) * 2;
+            uint32_t b0 = 0, b1 = 0;
+            if (g < MP) b0 = lds32(from), b1 = lds32(from + 16);
+            mma_bf16(c_co, a0, a1, a2, a3, b0, b1);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            uint32_t b0 = 0;
+            if (g < MP) b0 = lds32(sb + (j * MP * sx_row + st * kSums<G>) * 2);
+            mma_bf16_k8(c_co, a0, a1, b0);
+          }
         }
+      }
+      slot = slot == (STAGES - 1) * kStage ? 0 : slot + kStage;
+      if ((st & last) == last || st + 1 == nst) chunk = chunk == (STAGES - 1) * kChunk ? 0 : chunk + kChunk;
+      auto group = [&](int gi) {
         uint32_t a0[kWords], a1[kWords];
         lds_words<kWords>(a0, rp + (flip ^ (gi * kFlip)));
         lds_words<kWords>(a1, rp + (flip ^ (gi * kFlip)) + 8 * kRow);
@@ -281,18 +307,18 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
           mma_bf16(c, pair_of<0>(a0[i]), pair_of<0>(a1[i]), pair_of<1>(a0[i]), pair_of<1>(a1[i]), b.x, b.y);
           mma_bf16(c, pair_of<2>(a0[i]), pair_of<2>(a1[i]), pair_of<3>(a0[i]), pair_of<3>(a1[i]), b.z, b.w);
         }
-        const float s0 = __uint_as_float(gi & 1 ? s_lo & 0xffff0000u : s_lo << 16);
-        const float s1 = __uint_as_float(gi & 1 ? s_hi & 0xffff0000u : s_hi << 16);
+        const float s0 = __uint_as_float(gi & 1 ? s0w[gi / 2] & 0xffff0000u : s0w[gi / 2] << 16);
+        const float s1 = __uint_as_float(gi & 1 ? s1w[gi / 2] & 0xffff0000u : s1w[gi / 2] << 16);
         acc[0] = fmaf(s0, c[0], acc[0]);
         acc[1] = fmaf(s0, c[1], acc[1]);
         acc[2] = fmaf(s1, c[2], acc[2]);
         acc[3] = fmaf(s1, c[3], acc[3]);
       };
-      const int ngs = g1 - g0 - st * kGps;
+      const int ngs = NG - (st0 + st) * kGps;
       if (ngs >= kGps) {
 #pragma unroll
         for (int gi = 0; gi < kGps; ++gi) group(gi);
-      } else {  // the end of the range
+      } else {  // the end of the row
 #pragma unroll
         for (int gi = 0; gi < kGps - 1; ++gi)
           if (gi < ngs) group(gi);
@@ -305,10 +331,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int m = 2 * t + (r & 1);
-      if (m < MP) rw[m * kTile + 8 * (r >> 1)] = acc[r] + (AFFINE ? fmaf(8.f, c_sc[r], c_of[r]) : 0.f);
+      if (m < MP) rw[m * kTile + 8 * (r >> 1)] = acc[r] + (AFFINE ? c_co[r] : 0.f);
     }
     if (p.kw == 1) __syncwarp();
-    else if (p.kw == WARPS) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(p.kw * 32) : "memory");
     for (int i = kp * 32 + lane; i < MP * kTile; i += p.kw * 32) {
       const int m = i / kTile, row = (step * tps + sub) * kTile + i % kTile;
@@ -335,21 +360,23 @@ int32_t check_q4(const nslm_q4_matrix *W) {
 constexpr size_t kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of an SM, and of that for each CTA
 
 // Splits the work for CTAs of `warps` and gives their shared memory.
-size_t q4_plan(Q4Params &p, int mp, int warps, int stages) {
-  // the split of K with the least rounds of work: stages of 256 weights a warp,
-  // and what a tile costs besides (scales, sums, barrier), about one of them
+template <int G, bool AFFINE> size_t q4_plan(Q4Params &p, int mp, int warps, int stages) {
+  // the split of K with the least rounds of work: stages of a warp, and what a
+  // tile costs besides (sums, barrier), about one of them
   const int tiles = ceil_div(p.W.N, kTile), ctas = num_sms() * (warps == 8 ? 2 : 1);
+  // scales 16 bytes at once if there is a tile for every warp
+  p.spc = p.W.K % (8 * p.W.group) == 0 && tiles >= ctas * warps ? 8 / kGroups<G> : 1;
+  const int units = ceil_div(p.NS, p.spc);
   int64_t best = INT64_MAX;
-  for (int kw = warps; kw >= 1; kw /= 2) {
-    if (kw > p.NG) continue;
+  for (int kw = warps; kw >= 1; --kw) {
+    if (kw > units) continue;
     const int64_t rounds = ceil_div(ceil_div(tiles, warps / kw), ctas);
-    const int64_t cost = rounds * (ceil_div(ceil_div(p.NG, kw) * p.W.group, kStageK) + 1);
+    const int64_t cost = rounds * (ceil_div(units, kw) * p.spc + 1);
     if (cost < best) best = cost, p.kw = kw;
   }
   p.steps = ceil_div(tiles, warps / p.kw);
-  p.pos = p.kw * 16 * ceil_div(ceil_div(p.NG, p.kw), 16);
-  return kZero + (size_t)2 * mp * p.W.K + (p.W.biases ? (size_t)6 * mp * (p.pos + 8) : 0) +
-         (size_t)warps * stages * kStage + (size_t)2 * warps * kMaxVec * kTile * 4;
+  return kZero + (size_t)2 * mp * p.W.K + (AFFINE ? ((size_t)6 * mp * (p.NS * kSums<G> + 8) + 127) / 128 * 128 : 0) +
+         (size_t)warps * stages * kSlot<AFFINE> + (size_t)2 * warps * kMaxVec * kTile * 4;
 }
 
 template <int G, int MP, int WARPS, int STAGES, bool AFFINE>
@@ -371,17 +398,19 @@ int32_t launch_q4_as(const Q4Params &p, size_t smem, cudaStream_t s) {
 }
 
 // Two CTAs of 8 warps on an SM where the activations leave room for both, else
-// one of 16, with a shorter ring for the longest rows.
+// one of 16, or of 14 or 12 with a shorter ring for the longest rows.
 template <int G, int MP, bool AFFINE>
 int32_t launch_q4(Q4Params p, cudaStream_t s) {
-  size_t smem = q4_plan(p, MP, 8, 5);
-  if (2 * (smem + kSmemReserved) <= kSmemPerSm) return launch_q4_as<G, MP, 8, 5, AFFINE>(p, smem, s);
-  smem = q4_plan(p, MP, 8, 3);
+  size_t smem = q4_plan<G, AFFINE>(p, MP, 8, 4);
+  if (2 * (smem + kSmemReserved) <= kSmemPerSm) return launch_q4_as<G, MP, 8, 4, AFFINE>(p, smem, s);
+  smem = q4_plan<G, AFFINE>(p, MP, 8, 3);
   if (2 * (smem + kSmemReserved) <= kSmemPerSm) return launch_q4_as<G, MP, 8, 3, AFFINE>(p, smem, s);
-  smem = q4_plan(p, MP, 16, 4);
-  if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 16, 4, AFFINE>(p, smem, s);
-  smem = q4_plan(p, MP, 16, 2);
-  return launch_q4_as<G, MP, 16, 2, AFFINE>(p, smem, s);
+  smem = q4_plan<G, AFFINE>(p, MP, 16, 3);
+  if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 16, 3, AFFINE>(p, smem, s);
+  smem = q4_plan<G, AFFINE>(p, MP, 14, 2);
+  if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 14, 2, AFFINE>(p, smem, s);
+  smem = q4_plan<G, AFFINE>(p, MP, 12, 2);
+  return launch_q4_as<G, MP, 12, 2, AFFINE>(p, smem, s);
 }
 
 template <int G, int MP>
@@ -413,7 +442,7 @@ extern "C" int32_t nslm_q4_gemv(const nslm_q4_matrix *W, const uint16_t *x_bf16,
   if (!aligned16(x_bf16) || !aligned16(y)) return NSLM_ERR_ALIGN;
   if ((st = check_device())) return st;
   if (W->N == 0) return NSLM_OK;
-  Q4Params p{*W, x_bf16, y, M, W->K / W->group, 1, 0, 0, (flags & NSLM_GEMV_FIELDS_READY) != 0};
+  Q4Params p{*W, x_bf16, y, M, W->K / W->group, ceil_div(W->K, kStageK), 1, 0, 1, (flags & NSLM_GEMV_FIELDS_READY) != 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = W->group == 32 ? launch_q4<32>(p, s) : W->group == 64 ? launch_q4<64>(p, s) : launch_q4<128>(p, s);
   if (st == NSLM_OK) g_launches = 1;
