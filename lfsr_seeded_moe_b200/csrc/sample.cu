@@ -33,8 +33,12 @@ struct SampleParams {
   float *prob;
 };
 
-// A cluster of up to 8 CTAs has one row, each CTA a part of it, which it reads
-// once and keeps in shared memory as fp32.  w is 64-bit fixed point with 44 bits
+// A cluster of up to 8 CTAs has one row, each CTA a part of it.  While there are
+// SMs for more CTAs, a CTA reads its part once and keeps it in shared memory as
+// fp32 (RES).  Of a larger batch it takes a longer part, which passes through
+// small rings of its warps each time it is needed, from the L2 after the first:
+// then a row's barriers, about 1 us each, are shared by more logits, and the
+// whole batch runs at once.  w is 64-bit fixed point with 44 bits
 // behind the point, at most 2^18 of them, so sums stay below 2^62 and are
 // exact: whatever order threads and CTAs add in, the same u gives the same
 // token.
@@ -44,7 +48,9 @@ struct SampleParams {
 // P. T. P. Tang, "Table-driven implementation of the exponential function in
 // IEEE floating-point arithmetic", ACM TOMS 15, 1989): off by at most
 // r^6 / 720 = 2^-43 of itself.  A 16-entry table lies in 32 banks, so lanes
-// never wait for one another.
+// never wait for one another.  A pass is bound by its instructions, about 45 a
+// logit: with k from fp32 beside the fp64 operations, or the series in pairs
+// of terms, it takes more of them (32 us for 64 x 131072 logits, 34 and 35).
 struct Weight {
   float m;       // the row's largest logit
   float low;     // 40 temperatures below, where weights have long been 0: what is lower is not looked at
@@ -64,7 +70,7 @@ struct Weight {
     e = fma(e, r, 0x1.62e42fefa39efp-5);
     e = fma(e, r, 1.);
     const double w = e * pow16[k & 15];
-    return v >= low ? __hiloint2double(__double2hiint(w) + ((k >> 4) << 20), __double2loint(w)) : 0.;
+    return v >= low ? __hiloint2double(__double2hiint(w) + ((k & ~15) << 16), __double2loint(w)) : 0.;
   }
   __device__ __forceinline__ uint64_t fixed(float v) const { return to_fixed((*this)(v)); }
   // to the nearest integer: below 2^51 it stands in the low bits of w + 2^52
@@ -154,15 +160,22 @@ struct Range {
   __device__ __forceinline__ bool has(float v) const { return v >= lo && v < top && (bin < 0 || bin_of(v) == bin); }
 };
 
-struct Row {
+// NaN is never drawn.
+__device__ __forceinline__ float logit_of(float v) { return fmaxf(v, -INFINITY); }
+__device__ __forceinline__ float logit_of(__nv_bfloat16 v) { return logit_of(__bfloat162float(v)); }
+
+constexpr int kRing = 4, kRingChunk = 1024;  // chunks of a warp's ring, and their bytes
+
+template <class T, bool RES> struct Row {
   Shared &s;
-  const float *l;  // shared: this CTA's logits
+  const float *l;  // RES: this CTA's logits, in shared memory; else the CTA's rings
+  const T *src;    // and in global memory
   int n;           // how many
   int first;       // the index of the first
   int rank, ctas;  // in the cluster
   int warp, lane;
   int parity = 0;
-  float temp = 1.f;
+  bool infinite = false;  // +inf occurs: those are 0, all others -inf
   Weight w{};
   // the last token that stays, in the order of descending logits and ascending indexes
   float last_v = -INFINITY;
@@ -175,15 +188,75 @@ struct Row {
   // A warp's share of the CTA's logits: contiguous, so that sums over warps are sums over indexes.
   __device__ __forceinline__ int share() const { return ((n + kWarps - 1) / kWarps + 31) & ~31; }
 
-  // f(i, logit) for this thread's logits, U at a time so that their latencies
-  // overlap; i of a place past the end is meaningless, its logit -inf.
+  __device__ __forceinline__ float value(float v) const {
+    return infinite ? (v == INFINITY ? 0.f : -INFINITY) : v;
+  }
+  __device__ __forceinline__ float at(int i) const { return RES ? l[i] : value(logit_of(src[i])); }
+
+  // f(i, logit) for this thread's logits, U at a time so that their latencies overlap.
   template <int U, class F> __device__ __forceinline__ void each(F f) const {
-    for (int i = threadIdx.x; i < n; i += U * kThreads) {
-      float v[U];
+    if constexpr (RES) {
+      int i = threadIdx.x;
+      for (; i + (U - 1) * kThreads < n; i += U * kThreads) {
+        float v[U];
 #pragma unroll
-      for (int j = 0; j < U; ++j) v[j] = i + j * kThreads < n ? l[i + j * kThreads] : -INFINITY;
+        for (int j = 0; j < U; ++j) v[j] = l[i + j * kThreads];
 #pragma unroll
-      for (int j = 0; j < U; ++j) f(i + j * kThreads, v[j]);
+        for (int j = 0; j < U; ++j) f(i + j * kThreads, v[j]);
+      }
+#pragma unroll 1
+      for (; i < n; i += kThreads) f(i, l[i]);
+    } else {
+      // the warp's share by 16-byte copies from the last aligned address before
+      // it; bytes past its end are zeros
+      constexpr int kOf = kRingChunk / sizeof(T);
+      const int lo = min(n, warp * share()), hi = min(n, lo + share());
+      const int before = (int)(((uintptr_t)(src + lo) & 15) / sizeof(T));
+      const char *from = reinterpret_cast<const char *>(src + lo - before);
+      const int bytes = lo < hi ? (before + hi - lo) * (int)sizeof(T) : 0;
+      const T *ring = reinterpret_cast<const T *>(l) + warp * kRing * kOf;
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring) + lane * 16;
+      auto load = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < kRingChunk; j += 512) {
+          const int off = c * kRingChunk + j + lane * 16;
+          if (off < bytes)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + c % kRing * kRingChunk + j),
+                         "l"(from + off), "r"(min(16, bytes - off))
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int c = 0; c < kRing - 1; ++c) load(c);
+      for (int c = 0; c * kRingChunk < bytes; ++c) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+        __syncwarp();
+        load(c + kRing - 1);
+        const T *in = ring + c % kRing * kOf;
+        const int i0 = lo + c * kOf - before;  // the index of its first
+        if (i0 >= lo && i0 + kOf <= hi && !infinite) {
+          for (int q = 2 * lane; q < kOf; q += 32 * U) {
+            float v[U];
+#pragma unroll
+            for (int j = 0; j < U; j += 2) {
+              if constexpr (sizeof(T) == 4) {
+                const float2 x = *reinterpret_cast<const float2 *>(in + q + 32 * j);
+                v[j] = logit_of(x.x), v[j + 1] = logit_of(x.y);
+              } else {
+                const uint32_t x = *reinterpret_cast<const uint32_t *>(in + q + 32 * j);
+                v[j] = logit_of(__uint_as_float(x << 16)), v[j + 1] = logit_of(__uint_as_float(x & 0xffff0000u));
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) f(i0 + q + 32 * (j & ~1) + (j & 1), v[j]);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = max(i0, lo) + lane; i < min(i0 + kOf, hi); i += 32) f(i, value(logit_of(in[i - i0])));
+        }
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
     }
   }
 
@@ -226,6 +299,23 @@ struct Row {
     }
   }
 
+  // A lane's part of the sum of f over its warp's share.
+  template <class F> __device__ __forceinline__ uint64_t over_share(F f) const {
+    uint64_t a = 0;
+    if constexpr (RES) {
+      const int hi = min(n, (warp + 1) * share());
+      int i = warp * share() + lane;
+      for (; i + 32 < hi; i += 64) {
+        const float x = l[i], y = l[i + 32];
+        a += f(i, x) + f(i + 32, y);
+      }
+      if (i < hi) a += f(i, l[i]);
+    } else {
+      each<2>([&](int i, float v) { a += f(i, v); });
+    }
+    return a;
+  }
+
   // The sum of the warps' values, in the first warp.
   __device__ __forceinline__ uint64_t cta_sum(const uint64_t (&v)[kWarps]) const {
     return warp == 0 ? warp_sum_of(lane < kWarps ? v[lane] : 0) : 0;
@@ -238,13 +328,15 @@ struct Row {
     const int per = share();
     auto sum = [&](int lo, int hi) {
       uint64_t a = 0;
-      for (int i = lo + lane; i < hi; i += 64) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) a += f(i + 32 * j, i + 32 * j < hi ? l[i + 32 * j] : -INFINITY);
+      int i = lo + lane;
+      for (; i + 32 < hi; i += 64) {
+        const float x = at(i), y = at(i + 32);
+        a += f(i, x) + f(i + 32, y);
       }
+      if (i < hi) a += f(i, at(i));
       return warp_sum_of(a);
     };
-    uint64_t mine = sum(warp * per, min(n, (warp + 1) * per));
+    uint64_t mine = warp_sum_of(over_share(f));
     if (lane == 0) s.warp_mass[warp] = mine;
     __syncthreads();
     const uint64_t v[1] = {cta_sum(s.warp_mass)};
@@ -259,23 +351,23 @@ struct Row {
     uint64_t left = target(all);
     if (left < before || left - before >= slot[0][rank]) return -1;
     left -= before;
-    int at = 0;
-    while (at < kWarps - 1 && left >= s.warp_mass[at]) left -= s.warp_mass[at++];
-    int lo = at * per, hi = min(n, lo + per);
-    if (per > 256) {  // all warps on that warp's logits
-      const int sub = (per / kWarps + 31) & ~31;
-      mine = sum(lo + warp * sub, min(hi, lo + (warp + 1) * sub));
+    int in = 0;
+    while (in < kWarps - 1 && left >= s.warp_mass[in]) left -= s.warp_mass[in++];
+    int lo = in * per, hi = min(n, lo + per);
+    for (int len = per; len > 256;) {  // all warps on that warp's logits, and again
+      len = (len / kWarps + 31) & ~31;
+      mine = sum(lo + warp * len, min(hi, lo + (warp + 1) * len));
       __syncthreads();
       if (lane == 0) s.warp_mass[warp] = mine;
       __syncthreads();
-      at = 0;
-      while (at < kWarps - 1 && left >= s.warp_mass[at]) left -= s.warp_mass[at++];
-      lo += at * sub;
-      hi = min(hi, lo + sub);
+      in = 0;
+      while (in < kWarps - 1 && left >= s.warp_mass[in]) left -= s.warp_mass[in++];
+      lo += in * len;
+      hi = min(hi, lo + len);
     }
-    if (warp != at) return -1;
+    if (warp != in) return -1;
     for (int i = lo; i < hi; i += 32) {
-      const uint64_t upto = warp_scan_of(f(i + lane, i + lane < hi ? l[i + lane] : -INFINITY), lane);
+      const uint64_t upto = warp_scan_of(f(i + lane, i + lane < hi ? at(i + lane) : -INFINITY), lane);
       const uint32_t over = __ballot_sync(0xffffffffu, upto > left);
       if (over) return i + __ffs(over) - 1;
       left -= __shfl_sync(0xffffffffu, upto, 31);
@@ -449,16 +541,12 @@ struct Last {
   float v;
   int i, parity;
 };
-__device__ __noinline__ Last cut_row(Row r, uint64_t need, bool by_mass, Range range) {
+template <class T, bool RES> __device__ __noinline__ Last cut_row(Row<T, RES> r, uint64_t need, bool by_mass, Range range) {
   r.cut(need, by_mass, range);
   return Last{r.last_v, r.last_i, r.parity};
 }
 
-// NaN is never drawn.
-__device__ __forceinline__ float logit_of(float v) { return fmaxf(v, -INFINITY); }
-__device__ __forceinline__ float logit_of(__nv_bfloat16 v) { return logit_of(__bfloat162float(v)); }
-
-template <class T>
+template <class T, bool RES>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ float4 smem[];
   Shared &s = *reinterpret_cast<Shared *>(smem);
@@ -470,49 +558,51 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // 16-byte loads from the first aligned address on; the shared copy is shifted so that its stores are aligned too
   const T *src = reinterpret_cast<const T *>(p.logits) + (size_t)row * p.ld + first;
-  constexpr int kVec = 16 / sizeof(T);
-  const int head = min(n, (int)((-(uintptr_t)src & 15) / sizeof(T)));
-  float *l = reinterpret_cast<float *>(&s + 1) + (-head & 3);
+  float *l = reinterpret_cast<float *>(&s + 1);
   float hi = -INFINITY;
-  auto put = [&](float v) {
-    hi = fmaxf(hi, v);
-    return v;
-  };
-  const int vecs = (n - head) / kVec;
+  if constexpr (RES) {
+    // 16-byte loads from the first aligned address on; the shared copy is
+    // shifted so that its stores are aligned too
+    constexpr int kVec = 16 / sizeof(T);
+    const int head = min(n, (int)((-(uintptr_t)src & 15) / sizeof(T)));
+    l += -head & 3;
+    auto put = [&](float v) {
+      hi = fmaxf(hi, v);
+      return v;
+    };
+    const int vecs = (n - head) / kVec;
 #pragma unroll 4
-  for (int i = tid; i < vecs; i += kThreads) {
-    const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(src + head) + i);
-    float4 *dst = reinterpret_cast<float4 *>(l + head) + i * (kVec / 4);
-    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
-    if constexpr (sizeof(T) == 4) {
-      float f[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = put(logit_of(__uint_as_float(x[j])));
-      dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-    } else {
-      float f[8];
+    for (int i = tid; i < vecs; i += kThreads) {
+      const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(src + head) + i);
+      float4 *dst = reinterpret_cast<float4 *>(l + head) + i * (kVec / 4);
+      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+      float f[kVec];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        f[2 * j] = put(logit_of(__uint_as_float(x[j] << 16)));
-        f[2 * j + 1] = put(logit_of(__uint_as_float(x[j] & 0xffff0000u)));
+        if constexpr (sizeof(T) == 4) {
+          f[j] = put(logit_of(__uint_as_float(x[j])));
+        } else {
+          f[2 * j] = put(logit_of(__uint_as_float(x[j] << 16)));
+          f[2 * j + 1] = put(logit_of(__uint_as_float(x[j] & 0xffff0000u)));
+        }
       }
-      dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-      dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+      for (int j = 0; j < kVec; j += 4) dst[j / 4] = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+    }
+    if (tid < head) l[tid] = put(logit_of(src[tid]));
+    if (tid < n - head - vecs * kVec) {
+      const int i = head + vecs * kVec + tid;
+      l[i] = put(logit_of(src[i]));
     }
   }
-  if (tid < head) l[tid] = put(logit_of(src[tid]));
-  if (tid < n - head - vecs * kVec) {
-    const int i = head + vecs * kVec + tid;
-    l[i] = put(logit_of(src[i]));
-  }
+  Row<T, RES> r{s, l, src, n, first, rank, ctas, tid >> 5, tid & 31};
+  if constexpr (!RES) r.template each<4>([&](int, float v) { hi = fmaxf(hi, v); });
 
   const float temp = p.temperature ? p.temperature[row] : 1.f;
   const int top_k = p.top_k ? p.top_k[row] : 0;
   const float top_p = p.top_p ? p.top_p[row] : 1.f, u = p.u[row], q = p.min_p ? p.min_p[row] : 0.f;
   const bool greedy = !(temp > 0.f), by_count = !greedy && top_k > 0 && top_k < p.V, by_mass = !greedy && top_p < 1.f;
-  Row r{s, l, n, first, rank, ctas, tid >> 5, tid & 31};
 
   // The largest logits of kGroups parts of the row, in every CTA: `width` threads have one.
   const int width = kThreads / kGroups * ctas;
@@ -560,13 +650,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (rank == 0 && tid == 0) put_out(-1, 0.f);
     return;
   }
-  const bool infinite = hi == INFINITY;
-  if (infinite) {  // only those are left, all alike
-    for (int i = tid; i < n; i += kThreads) l[i] = l[i] == INFINITY ? 0.f : -INFINITY;
-    __syncthreads();
+  r.infinite = hi == INFINITY;
+  if (r.infinite) {  // only those are left, all alike
+    if constexpr (RES) {
+      for (int i = tid; i < n; i += kThreads) l[i] = r.value(l[i]);
+      __syncthreads();
+    }
     hi = 0.f;
   }
-  r.temp = temp;
   r.w = Weight{hi, fmaxf(__fmaf_rn(-40.f, temp, hi), -FLT_MAX), 16. / (0.69314718055994530942 * (double)temp), s.pow16};
   const double min_w = q > 0.f ? fmin((double)q, 1.) * 0x1p44 : 0.;
   auto target = [&](uint64_t all) -> uint64_t {
@@ -580,14 +671,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   uint64_t all_mass = 0, list_mass = 0;  // of the row, and from list_from on
   float list_from = INFINITY;
   if (by_count || by_mass) {
-    const float from = p.V <= kList || infinite ? -FLT_MAX : fmaxf(s.list_from, -FLT_MAX);
+    const float from = p.V <= kList || r.infinite ? -FLT_MAX : fmaxf(s.list_from, -FLT_MAX);
     uint64_t sum[2] = {0, 0};
     if (by_count) {
-      r.each<4>([&](int i, float v) {
+      r.template each<4>([&](int i, float v) {
         if (v >= from) r.add_to_list(i, v);
       });
     } else {
-      r.each<2>([&](int i, float v) {
+      r.template each<2>([&](int i, float v) {
         sum[0] += r.w.fixed(v);
         if (v >= from) r.add_to_list(i, v);
       });
@@ -598,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (!by_count) sum[0] = r.cta_sum(s.warp_mass);
     sum[1] = (uint64_t)s.list_n;
     const auto slot = r.publish(sum);
-    const int len = r.gather(slot[1]), per = Row::threads_each(len), c = tid / per;
+    const int len = r.gather(slot[1]), per = Row<T, RES>::threads_each(len), c = tid / per;
     for (int k = 0; k < ctas; ++k) all_mass += slot[0][k];
     // CTA 0 puts the list in order: a token's place, and the mass before it
     uint64_t good[2] = {0, 0}, need = 0, before = 0;
@@ -662,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       cut(top_k, false);
       if (by_mass) {
         uint64_t sum[1] = {0};
-        r.each<2>([&](int i, float v) {
+        r.template each<2>([&](int i, float v) {
           if (v >= r.last_v && r.kept(i, v)) sum[0] += r.w.fixed(v);
         });
         sum[0] = warp_sum_of(sum[0]);
@@ -698,20 +789,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   } else {
     at = r.find([&](int, float v) { return r.w.fixed(v); }, target, Z);
   }
-  if (at >= 0 && r.lane == 0) put_out(first + at, greedy ? 1.f : (float)(r.w(l[at]) / (double)Z));
+  if (at >= 0 && r.lane == 0) put_out(first + at, greedy ? 1.f : (float)(r.w(r.at(at)) / (double)Z));
 }
 
-template <class T>
-int32_t launch_sample(SampleParams p, int32_t B, cudaStream_t s) {
-  // CTAs of a row: at most 16384 logits each where that is possible, and more
-  // of them while SMs are left and a CTA keeps 2048 logits
-  int ctas = 1;
-  while (ctas < kMaxCluster && (ceil_div(p.V, ctas) > 16384 ||
-                                ((int64_t)B * ctas * 2 <= 2 * num_sms() && p.V / (2 * ctas) >= 2048)))
-    ctas *= 2;
-  p.len = ceil_div(ceil_div(p.V, ctas), 8) * 8;
-  const size_t smem = sizeof(Shared) + (size_t)(p.len + 8) * 4;
-  auto k = sample_kernel<T>;
+template <class T, bool RES> int32_t launch_sample(const SampleParams &p, int32_t B, int ctas, size_t smem, cudaStream_t s) {
+  auto k = sample_kernel<T, RES>;
   if (int32_t st = ensure_smem((const void *)k, smem)) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(B * ctas));
@@ -728,6 +810,26 @@ int32_t launch_sample(SampleParams p, int32_t B, cudaStream_t s) {
   cfg.numAttrs = 2;
   if (int32_t st = cuda_status(cudaLaunchKernelEx(&cfg, k, p))) return st;
   return launch_status();
+}
+
+template <class T> int32_t launch_sample(SampleParams p, int32_t B, cudaStream_t s) {
+  // CTAs of a row: at most 16384 logits each where that is possible, and more
+  // of them while SMs are left and a CTA keeps 2048 logits
+  const int slots = 2 * num_sms();  // CTAs that run at once: 512 threads of 64 registers
+  int ctas = 1;
+  while (ctas < kMaxCluster && (ceil_div(p.V, ctas) > 16384 ||
+                                ((int64_t)B * ctas * 2 <= slots && p.V / (2 * ctas) >= 2048)))
+    ctas *= 2;
+  auto part = [&] { return ceil_div(ceil_div(p.V, ctas), 8) * 8; };
+  p.len = part();
+  size_t smem = sizeof(Shared) + (size_t)(p.len + 8) * 4;
+  const int64_t at_once = 2 * smem <= 226 * 1024 ? slots : slots / 2;
+  if (B * (int64_t)ctas <= at_once) return launch_sample<T, true>(p, B, ctas, smem, s);
+  // more than run at once: longer parts
+  while (ctas > 1 && B * (int64_t)ctas > slots) ctas /= 2;
+  p.len = part();
+  smem = sizeof(Shared) + kWarps * kRing * kRingChunk;
+  return launch_sample<T, false>(p, B, ctas, smem, s);
 }
 
 }  // namespace
