@@ -165,13 +165,13 @@ int32_t nslm_seed_gemv_flags(const nslm_seed_matrix *W, const uint16_t *x_bf16, 
 /* GEMV from 4-bit weights, for the projections that stay outside the seed
  * format (router, output head, attention):
  *   y[m][i] = sum_k W[i][k] * x[m][k],  m < M, i < N.
- * x: bf16 [M][K]; y: fp32 [M][N]; 1 <= M <= 8; M, rounded up to 1, 2,
- * 4 or 8, times K is at most 65536 (the activations stay in shared memory).  Products are exact, sums are held in fp32; the
- * weights are never rounded.  Finite x.  flags: 0 or NSLM_GEMV_FIELDS_READY,
- * with the meaning of nslm_seed_gemv_flags (no kernel enqueued earlier on
- * `stream` writes W's q, scales or biases); other bits return NSLM_ERR_ARG.
- * The result does not depend on timing (no atomics).  One launch, no
- * workspace.  y must not overlap any input. */
+ * x: bf16 [M][K]; y: fp32 [M][N]; 1 <= M <= 8; M, rounded up to 1, 2, 4 or 8,
+ * times K is at most 65536 (the activations stay in shared memory).  Products
+ * are exact, sums are held in fp32; the weights are never rounded.  Finite x.
+ * flags: 0 or NSLM_GEMV_FIELDS_READY, with the meaning of nslm_seed_gemv_flags
+ * (no kernel enqueued earlier on `stream` writes W's q, scales or biases);
+ * other bits return NSLM_ERR_ARG.  The result does not depend on timing (no
+ * atomics).  One launch, no workspace.  y must not overlap any input. */
 int32_t nslm_q4_gemv(const nslm_q4_matrix *W, const uint16_t *x_bf16, int32_t M, float *y,
                      uint32_t flags, nslm_stream_t stream);
 
@@ -214,9 +214,9 @@ int32_t nslm_moe_route_topk(const float *logits, int32_t T, int32_t E, int32_t k
  * int32 [E + 1] or NULL, the counts' running sum from 0, as
  * nslm_seed_grouped_gemm takes them for rows grouped by expert; mean_p fp32
  * [E] or NULL; loss fp32 [1].  n = 0 (or T = 0) gives zeros.
- * 1 <= k <= 8, k <= E <= 1024.  Sums are taken in a fixed order: equal calls
- * give equal bits.  T <= 1024 takes one launch and no workspace (ws may be
- * NULL), larger T two.  Workspace:
+ * 1 <= k <= 8, k <= E <= 1024, T <= 2^28, T * k < 2^31.  Sums are taken in a
+ * fixed order: equal calls give equal bits.  T <= 1024 takes one launch and no
+ * workspace (ws may be NULL), larger T two.  Workspace:
  * nslm_workspace_bytes(NSLM_OP_MOE_BALANCE, T, E, 0, 0, k, 0). */
 int32_t nslm_moe_balance(const float *logits, const int32_t *ids, const uint8_t *mask, int32_t T,
                          int32_t E, int32_t k, float coef, int32_t *counts, int32_t *offsets,
@@ -269,8 +269,8 @@ typedef struct {
  * are left, equally likely.  A row with nothing left gives token -1, prob 0.
  * logits: [B] rows of V values of type `type`, `ld` >= V elements apart, only
  * read; u: fp32 [B]; token: int32 [B]; prob: fp32 [B] or NULL; params NULL:
- * plain sampling at temperature 1.  B >= 0, 1 <= V <= 262144.  One launch, no
- * workspace. */
+ * plain sampling at temperature 1.  0 <= B <= 2^24, 1 <= V <= 262144.  One
+ * launch, no workspace. */
 int32_t nslm_sample(const void *logits, int32_t type, int32_t B, int32_t V, int64_t ld,
                     const nslm_sample_params *params, const float *u, int32_t *token, float *prob,
                     nslm_stream_t stream);

@@ -407,7 +407,8 @@ int32_t launch(K k, int ctas, int cluster, int threads, size_t smem, cudaStream_
 }
 
 int32_t check_sizes(int32_t T, int32_t E, int32_t k) {
-  return T < 0 || k < 1 || k > 8 || E < k || E > kMaxE ? NSLM_ERR_SHAPE : NSLM_OK;
+  if (T < 0 || T > (1 << 28) || k < 1 || k > 8 || E < k || E > kMaxE) return NSLM_ERR_SHAPE;
+  return (int64_t)T * k > INT32_MAX ? NSLM_ERR_SHAPE : NSLM_OK;  // the counts are int32
 }
 
 }  // namespace

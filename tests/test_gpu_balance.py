@@ -255,3 +255,56 @@ def test_offsets_past_32_bits(nslm):
     # p5 by itself and in the dot product that is taken from 1
     assert bool(((d[-3:, 5] - want).abs() <= 2 * 96 * 2.0 ** -24 * E / 3 * p5 * (1 + p5)).all())
     assert bool((d[:-3] == 0).all())
+
+
+def test_graphs_that_share_a_workspace_and_calls_at_once(nslm):
+    # one workspace for two captured graphs of unlike sizes, replayed in turn (nothing in it outlives a call);
+    # two of its own for calls on two streams at once
+    E, k = 100, 8
+    z, ids = _inputs(6000, E, k, 41)
+    need = nslm.nslm_workspace_bytes(nslm.NSLM_OP_MOE_BALANCE, 6000, E, 0, 0, k)
+    ws = [guard.buffer(need, torch.uint8, fill=0xFF) for _ in range(2)]
+    out = [(guard.buffer(E + 1, torch.int32, fill=-1), guard.buffer(1, torch.float32)) for _ in range(2)]
+    sizes = (6000, 1100)
+    want = [_want(z[:T], ids[:T], None, E, k, 1.0) for T in sizes]
+
+    def call(i, w, stream=None):
+        nslm.nslm_moe_balance(z, ids, None, sizes[i], E, k, 1.0, out[i][0], None, None, out[i][1], w, need, stream)
+
+    def check():
+        for i, T in enumerate(sizes):
+            assert np.array_equal(out[i][0].cpu().numpy(), want[i][0])
+            assert abs(float(out[i][1]) - want[i][3]) <= (96 + T // 8) * 2.0 ** -24 * want[i][3]
+            out[i][0].fill_(-1), out[i][1].zero_()
+
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            call(i, ws[0])
+    for _ in range(3):
+        graphs[0].replay()
+        graphs[1].replay()
+        check()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            call(i, ws[i], streams[i])
+    torch.cuda.synchronize()
+    check()
+
+
+def test_gradient_through_a_graph_while_the_loss_is_used_eagerly(nslm):
+    # the gradient captured while an eager call of the same logits is under way: plain buffers, no state between
+    T, E, k = 1200, 40, 2
+    z, ids = _inputs(T, E, k, 42)
+    counts = _run(nslm, z, ids, None, E, k, 1.0)[0]
+    want = _grad(nslm, z, counts, None, k, 1.0, None)
+    d = guard.buffer((T, E), torch.float32, fill=float("nan"))
+    eager = guard.buffer((T, E), torch.float32, fill=float("nan"))
+    nslm.nslm_moe_balance_grad(z, counts, None, T, E, k, 1.0, None, eager)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nslm.nslm_moe_balance_grad(z, counts, None, T, E, k, 1.0, None, d)
+    g.replay()
+    assert torch.equal(d, want) and torch.equal(eager, want)

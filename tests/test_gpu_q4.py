@@ -78,6 +78,31 @@ def test_whole_numbers_are_equal(nslm, N, K, G, affine):
         assert torch.equal(y.double(), x.double() @ w.t()), M
 
 
+# enough rows for a tile a warp (their scales come 16 bytes at once where K is a
+# multiple of 8 groups), and rows so long that the activations take the room of
+# a second CTA, or of most warps
+LONG = [(40000, 512, 32, 1), (40001, 512, 64, 4), (38000, 1024, 128, 3), (39990, 1536, 64, 8), (40000, 1000 * 32, 32, 1),
+        (33153, 8192, 32, 8), (35000, 8192, 64, 8), (33200, 8192, 128, 5), (120, 16384, 32, 4), (700, 32768, 64, 2),
+        (19000, 16384, 64, 3), (2400, 65536, 128, 1), (37000, 7 * 256, 32, 6), (2500, 6000 // 32 * 32, 32, 7)]
+
+
+@pytest.mark.parametrize("affine", [True, False])
+@pytest.mark.parametrize("N,K,G,M", LONG)
+def test_many_rows_and_long_ones_are_equal(nslm, N, K, G, M, affine):
+    q, scales, biases = _weights(N, K, G, affine, N + K, True)
+    x = _x(M, K, N, True)
+    y = _run(nslm, q, scales, biases, G, x)
+    for i in range(0, N, 4096):
+        b = biases[i:i + 4096] if affine else None
+        w, _ = _dense(q[i:i + 4096], scales[i:i + 4096], b, G)
+        # any partial sum, however the offset is taken apart: halves below 2^22
+        size = 16 * scales[i:i + 4096].double().repeat_interleave(G, 1)
+        if affine:
+            size += b.double().abs().repeat_interleave(G, 1)
+        assert float((x.double().abs() @ size.t()).max()) < 2**22
+        assert torch.equal(y[:, i:i + 4096].double(), x.double() @ w.t()), i
+
+
 @pytest.mark.parametrize("N,K,G,M,affine", [(100, 1408, 128, 5, False), (512, 1024, 64, 1, True), (2048, 4096, 32, 1, True),
                                             (333, 8192, 64, 8, True), (1000, 2048, 32, 3, False), (64, 16384, 128, 4, True)])
 def test_random_numbers_within_rounding(nslm, N, K, G, M, affine):
@@ -183,3 +208,22 @@ def test_no_rows(nslm):
     nslm.nslm_q4_gemv(W, q, 1, y)
     assert nslm.nslm_last_launch_count() == 0
     assert bool((y == 7).all()) and np.isfinite(float(y.sum()))
+
+
+def test_two_calls_at_once(nslm):
+    # two streams, two outputs, one matrix and one x: calls share nothing that they write
+    N, K, G = 20000, 2048, 64
+    q, scales, biases = _weights(N, K, G, True, 61, True)
+    w, _ = _dense(q, scales, biases, G)
+    x = _x(8, K, 3, True)
+    want = x.double() @ w.t()
+    W = nslm.q4_matrix(q, scales, biases, G)
+    ys = [guard.buffer((8, N), torch.float32, fill=float("nan")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, y in zip(streams, ys):
+            nslm.nslm_q4_gemv(W, x, 8, y, nslm.NSLM_GEMV_FIELDS_READY, s)
+    torch.cuda.synchronize()
+    for y in ys:
+        assert torch.equal(y.double(), want)

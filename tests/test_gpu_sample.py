@@ -268,3 +268,68 @@ def test_offsets_past_32_bits(nslm):
     whole[:, :V] = _logits(B, V, 3, 3.0, torch.bfloat16)
     u = torch.rand(B, generator=_gen(1), device="cuda")
     _check(nslm, whole, u, V=V, top_p=_full(B, 0.9))
+
+
+# more rows than fit on the GPU at once: with one CTA a row, with two and more
+LARGE = [(310, 3001), (310, 40001), (100, 60001), (70, 131072), (40, 262143)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V", LARGE)
+def test_large_batches(nslm, B, V, dtype):
+    # rows at odd addresses, some with masked logits, some with nothing left
+    ld = V + 3
+    whole = torch.full((B, ld), 1e4, device="cuda", dtype=dtype)
+    l = whole[:, :V]
+    l.copy_(_logits(B, V, V, 3.0, dtype))
+    inf = float("inf")
+    l[5::17, ::2] = -inf
+    l[6::17, 1::3] = float("nan")
+    l[7] = -inf
+    l[8, V // 2:] = torch.finfo(dtype).min
+    l[9, [1, V // 3, V - 1]] = inf
+    l[10] = 0.0
+    l[11::17, :] *= 0.02                            # nearly even: the threshold is far down
+    l[12, :] = -inf
+    l[12, V - 1] = -2.0
+    u = torch.rand(B, generator=_gen(V), device="cuda")
+    t = 0.5 + torch.rand(B, generator=_gen(V + 1), device="cuda")
+    t[::31] = 0
+    ks = torch.randint(1, 3000, (B,), generator=_gen(V + 2), device="cuda").to(torch.int32)
+    few = torch.randint(1, 60, (B,), generator=_gen(V + 5), device="cuda").to(torch.int32)
+    ps = torch.rand(B, generator=_gen(V + 3), device="cuda")
+    ms = 0.3 * torch.rand(B, generator=_gen(V + 4), device="cuda")
+    _check(nslm, whole, u, V=V)
+    _check(nslm, whole, u, V=V, t=t, top_k=few, top_p=ps, min_p=ms)
+    _check(nslm, whole, u, V=V, t=t, top_k=ks, top_p=ps)
+    _check(nslm, whole, u, V=V, top_p=ps)
+
+
+def test_a_row_alone_and_in_a_large_batch_are_equal(nslm):
+    # a row's draw does not depend on how many rows are drawn with it
+    B, V = 80, 50257
+    l = _logits(B, V, 17, 2.0)
+    u = torch.rand(B, generator=_gen(3), device="cuda")
+    for kw in (dict(), dict(top_k=_full(B, 50, torch.int32)), dict(top_p=_full(B, 0.9))):
+        token, prob = _run(nslm, l, u, **kw)
+        for i in (0, 41, 79):
+            one = {n: v[:1] for n, v in kw.items()}
+            a, b = _run(nslm, l[i:i + 1].clone(), u[i:i + 1].clone(), **one)
+            assert a[0] == token[i] and b[0] == prob[i]
+
+
+def test_two_calls_at_once(nslm):
+    B, V = 48, 100000
+    l = _logits(B, V, 23, 2.0)
+    u = [torch.rand(B, generator=_gen(i), device="cuda") for i in range(2)]
+    p = _full(B, 0.9)
+    params = nslm.sample_params(None, None, p, None)
+    out = [guard.buffer(B, torch.int32, fill=-7) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            nslm.nslm_sample(l, nslm.NSLM_TYPE_F32, B, V, V, params, u[i], out[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert np.array_equal(out[i].cpu().numpy(), _want(l, u[i], top_p=p)[0])

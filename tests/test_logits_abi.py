@@ -53,7 +53,8 @@ def _balance(**kw):
 def test_balance_refusals():
     for kw in (dict(logits=0), dict(ids=0), dict(counts=0), dict(loss=0)):
         assert _balance(**kw) == nslm.NSLM_ERR_ARG, kw
-    for kw in (dict(T=-1), dict(k=0), dict(k=9, E=16), dict(E=1), dict(E=1025)):
+    for kw in (dict(T=-1), dict(k=0), dict(k=9, E=16), dict(E=1), dict(E=1025),
+               dict(T=2**28 + 1), dict(T=2**28, k=8)):
         assert _balance(**kw) == nslm.NSLM_ERR_SHAPE, kw
     for name in ("logits", "ids", "mask", "counts", "offsets", "mean_p", "loss"):
         assert _balance(**{name: A + 4}) == nslm.NSLM_ERR_ALIGN, name
@@ -75,7 +76,8 @@ def test_balance_grad_refusals():
 
     for kw in (dict(logits=0), dict(counts=0), dict(dlogits=0)):
         assert call(**kw) == nslm.NSLM_ERR_ARG, kw
-    for kw in (dict(T=-1), dict(k=0), dict(k=9, E=16), dict(E=1), dict(E=1025)):
+    for kw in (dict(T=-1), dict(k=0), dict(k=9, E=16), dict(E=1), dict(E=1025),
+               dict(T=2**28 + 1), dict(T=2**28, k=8)):
         assert call(**kw) == nslm.NSLM_ERR_SHAPE, kw
     for name in ("logits", "counts", "mask", "dloss", "dlogits"):
         assert call(**{name: A + 4}) == nslm.NSLM_ERR_ALIGN, name
@@ -91,7 +93,7 @@ def test_sample_refusals():
 
     for kw in (dict(logits=0), dict(u=0), dict(token=0), dict(type=2), dict(type=-1)):
         assert call(**kw) == nslm.NSLM_ERR_ARG, kw
-    for kw in (dict(B=-1), dict(V=0), dict(V=262145, ld=262145), dict(ld=99)):
+    for kw in (dict(B=-1), dict(V=0), dict(V=262145, ld=262145), dict(ld=99), dict(B=2**24 + 1)):
         assert call(**kw) == nslm.NSLM_ERR_SHAPE, kw
     for name in ("logits", "u", "token", "prob"):
         assert call(**{name: A + 4}) == nslm.NSLM_ERR_ALIGN, name
