@@ -111,7 +111,8 @@ struct alignas(16) Shared {
       uint32_t lo[kBins], hi[kBins];
     } hist;
     struct {
-      Candidate mine[kList], list[kList];  // the CTA's part, and in CTA 0 all
+      Candidate mine[kList], list[kList], sorted[kList];  // the CTA's part, and in CTA 0 all
+      int32_t place[kList];                               // of the sorted, by their indexes
     };
   };
 };
@@ -396,16 +397,41 @@ template <class T, bool RES> struct Row {
     __syncthreads();
     return total;
   }
-  // The sum of f over the list, in each of `per` threads.
-  template <class F> __device__ __forceinline__ uint64_t over_list(int n, int per, F f) {
-    uint64_t a = 0;
-#pragma unroll 4
-    for (int j = threadIdx.x & (per - 1); j < n; j += per) a += f(s.list[j]);
-    for (int o = 1; o < per; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    return a;
+  // The sum of the threads' values before this one's, and of all.
+  __device__ __forceinline__ uint64_t sum_before(uint64_t v, uint64_t &all) const {
+    const uint64_t upto = warp_scan_of(v, lane);
+    __syncthreads();
+    if (lane == 31) s.warp_mass[warp] = upto;
+    __syncthreads();
+    uint64_t before = upto - v;
+    all = 0;
+#pragma unroll
+    for (int k = 0; k < kList / 32; ++k) {  // only those threads have any
+      const uint64_t x = s.warp_mass[k];
+      before += k < warp ? x : 0;
+      all += x;
+    }
+    return before;
   }
-  // threads for each of n candidates
-  __device__ __forceinline__ static int threads_each(int n) { return n <= 64 ? 8 : n <= 128 ? 4 : 2; }
+  // Thread j gets the j-th of the list's n in their order.  Each candidate's
+  // place is the number of those before it, counted by up to 8 threads: 65536
+  // comparisons at most, of 4 instructions; sums in the same loop took 12.
+  __device__ __forceinline__ Candidate sorted(int n) {
+    const int per = n <= 64 ? 8 : n <= 128 ? 4 : 2, c = threadIdx.x / per;
+    const Candidate x = s.list[min(c, n - 1)];
+    int order = 0, place = 0;
+#pragma unroll 4
+    for (int j = threadIdx.x & (per - 1); j < n; j += per) {
+      const uint64_t key = s.list[j].key;
+      order += key > x.key;
+      place += (uint32_t)key > (uint32_t)x.key;
+    }
+    order |= place << 16;
+    for (int o = 1; o < per; o <<= 1) order += __shfl_xor_sync(0xffffffffu, order, o);
+    if (c < n && threadIdx.x % per == 0) s.sorted[order & 0xffff] = x, s.place[order & 0xffff] = order >> 16;
+    __syncthreads();
+    return s.sorted[min((int)threadIdx.x, n - 1)];
+  }
 
   // Sets the last token that stays to the one at which the kept tokens' count
   // (by_mass: their mass), in their order, first reaches `need`.  r: where it
@@ -433,20 +459,18 @@ template <class T, bool RES> struct Row {
       });
       sync_row();
       // each CTA adds its part of all histograms
+      // (kBins / ctas bins of all; always kPer values a thread, so that their
+      // reads run at once: one after another they took 17000 cycles)
       constexpr int kPer = kBins / kThreads;
-      const int per = kPer / ctas, b0 = rank * (kBins / ctas) + threadIdx.x * per;
-      uint64_t x[kPer] = {}, sum = 0;
+      const int log = __ffs(ctas) - 1, b0 = (rank * kThreads + threadIdx.x) * kPer >> log;
+      uint64_t x[kPer], sum = 0;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        if (q >= per) break;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) {
-          if (k >= ctas) break;
-          const Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, k);
-          x[q] += ((uint64_t)o->hist.hi[b0 + q] << 32) + o->hist.lo[b0 + q];
-        }
-        sum += x[q];
+        const Shared *o = cg::this_cluster().map_shared_rank(&s, q & (ctas - 1));
+        x[q] = (uint64_t)o->hist.hi[b0 + (q >> log)] << 32 | o->hist.lo[b0 + (q >> log)];
       }
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) sum += x[q];
       uint64_t upto = warp_scan_of(sum, lane);
       if (lane == 31) s.warp_mass[warp] = upto;
       __syncthreads();
@@ -462,11 +486,14 @@ template <class T, bool RES> struct Row {
       for (int k = 0; k < warp; ++k) upto += s.warp_mass[k];
       if (threadIdx.x == 0) s.found = -1, s.list_n = 0;
       __syncthreads();
+      sum = 0;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        if (q >= per) break;
-        if (upto < need && need <= upto + x[q]) s.found = b0 + q, s.found_mass = upto;
-        upto += x[q];
+        sum += x[q];
+        if ((q + 1) & (ctas - 1)) continue;  // the bin goes on
+        if (upto < need && need <= upto + sum) s.found = b0 + (q >> log), s.found_mass = upto;
+        upto += sum;
+        sum = 0;
       }
       __syncthreads();
       const uint64_t mine[2] = {(uint64_t)(s.found + 1), s.found >= 0 ? s.found_mass : 0};
@@ -518,11 +545,11 @@ template <class T, bool RES> struct Row {
     const int len = gather(publish(count)[0]);
     uint64_t found[1] = {0};  // the token's key
     if (rank == 0 && len <= kList) {
-      const int per = threads_each(len), c = threadIdx.x / per;
-      const Candidate x = s.list[min(c, len - 1)];
-      const uint64_t before =
-          r.above + over_list(len, per, [&](const Candidate &y) { return y.key > x.key ? (by_mass ? y.w : 1) : 0; });
-      if (c < len && before < need && need <= before + (by_mass ? x.w : 1)) s.found_mass = x.key;
+      const Candidate x = sorted(len);
+      const uint64_t w = threadIdx.x >= len ? 0 : by_mass ? x.w : 1;
+      uint64_t all;
+      const uint64_t before = r.above + sum_before(w, all);
+      if (before < need && need <= before + w) s.found_mass = x.key;
       __syncthreads();
       found[0] = s.found_mass;
     }
@@ -689,24 +716,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (!by_count) sum[0] = r.cta_sum(s.warp_mass);
     sum[1] = (uint64_t)s.list_n;
     const auto slot = r.publish(sum);
-    const int len = r.gather(slot[1]), per = Row<T, RES>::threads_each(len), c = tid / per;
+    const int len = r.gather(slot[1]);
     for (int k = 0; k < ctas; ++k) all_mass += slot[0][k];
     // CTA 0 puts the list in order: a token's place, and the mass before it
-    uint64_t good[2] = {0, 0}, need = 0, before = 0;
-    int order = kList;
+    uint64_t good[2] = {0, 0}, need = 0, before = 0, Z;
     Candidate x{};
-    float v = 0.f;
     if (rank == 0 && len <= kList) {
-      x = s.list[min(c, len - 1)];
-      v = x.logit();
-      // their count above bit 53 (at most 2^8 weights of at most 2^44)
-      const uint64_t ahead = r.over_list(len, per, [&](const Candidate &y) {
-        return y.key > x.key ? y.w | 1ull << 53 : 0;
-      });
-      if (c < len) order = (int)(ahead >> 53);
-      before = ahead & ((1ull << 53) - 1);
-      if (order == (by_count ? min(top_k, len) : len) - 1) s.found_mass = before + x.w;
-      if (order == len - 1) s.found = r.w(v) < min_w || p.V <= kList;
+      x = r.sorted(len);
+      before = r.sum_before(tid < len ? x.w : 0, Z);
+      if (tid == (by_count ? min(top_k, len) : len) - 1) s.found_mass = before + x.w;
+      if (tid == len - 1) s.found = r.w(x.logit()) < min_w || p.V <= kList;
       __syncthreads();
       // all that stays is in the list if its end is behind top-k's, top-p's or min-p's
       const bool whole = s.found || (by_count && len >= top_k);
@@ -719,23 +738,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     list_mass = told[1][0];
     if (told[0][0]) {
       if (rank != 0) return;
-      // tokens that stay: of the first top_k, those with less than need before them that min-p leaves
-      const bool stays = c < len && order < (by_count ? top_k : kList) && before < need && (order == 0 || r.w(v) >= min_w);
-      if (c < len && tid % per == 0) s.list[c].w = stays ? x.w : 0;
+      // tokens that stay: of the first top_k, those with less than need before them that min-p leaves;
+      // then all by their indexes
+      const bool stays = tid < (by_count ? min(top_k, len) : len) && before < need && (tid == 0 || r.w(x.logit()) >= min_w);
+      if (tid < len) s.list[s.place[tid]] = Candidate{x.key, stays ? x.w : 0};
       __syncthreads();
-      uint64_t Z = 0, below = 0;
-#pragma unroll 4
-      for (int j = tid & (per - 1); j < len; j += per) {
-        const Candidate y = s.list[j];
-        Z += y.w;
-        below += (uint32_t)y.key > (uint32_t)x.key ? y.w : 0;
-      }
-      for (int o = 1; o < per; o <<= 1) {
-        Z += __shfl_xor_sync(0xffffffffu, Z, o);
-        below += __shfl_xor_sync(0xffffffffu, below, o);
-      }
-      const uint64_t at = target(Z);
-      if (tid % per == 0 && stays && below <= at && at < below + x.w) put_out(x.index(), (float)(r.w(v) / (double)Z));
+      if (tid < len) x = s.list[tid];
+      const uint64_t w = tid < len ? x.w : 0, below = r.sum_before(w, Z), at = target(Z);
+      if (below <= at && at < below + w) put_out(x.index(), (float)(r.w(x.logit()) / (double)Z));
       return;
     }
   }

@@ -148,14 +148,19 @@ def _p(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
+
+
+_torch = None  # imported by the first call that needs the current stream
 
 
 def _s(stream) -> int:
     if stream is None:
-        import torch
+        global _torch
+        if _torch is None:
+            import torch as _torch
         # the handle alone: current_stream() builds a Stream object, 3 us of a call's 8
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -221,7 +226,7 @@ def q4_matrix(q, scales, biases, group: int) -> nslm_q4_matrix:
 
 def nslm_q4_gemv(W, x_bf16, M: int, y, flags: int = 0, stream=None) -> None:
     """W: an nslm_q4_matrix (see q4_matrix)."""
-    _check("nslm_q4_gemv", _lib.nslm_q4_gemv(ctypes.byref(W), _p(x_bf16), M, _p(y), int(flags), _s(stream)))
+    _check("nslm_q4_gemv", _lib.nslm_q4_gemv(W, _p(x_bf16), M, _p(y), flags, _s(stream)))
 
 
 def nslm_seed_grouped_gemm(W, E: int, x_bf16, offsets, R: int, y, ws=None, ws_bytes: int = 0,
@@ -258,8 +263,7 @@ def sample_params(temperature=None, top_k=None, top_p=None, min_p=None) -> nslm_
 def nslm_sample(logits, type: int, B: int, V: int, ld: int, params, u, token, prob=None, stream=None) -> None:
     """params: an nslm_sample_params (see sample_params) or None."""
     _check("nslm_sample",
-           _lib.nslm_sample(_p(logits), type, B, V, ld, None if params is None else ctypes.byref(params), _p(u),
-                            _p(token), _p(prob), _s(stream)))
+           _lib.nslm_sample(_p(logits), type, B, V, ld, params, _p(u), _p(token), _p(prob), _s(stream)))
 
 
 def nslm_moe_seed_ffn(gate, up, down, E: int, x_bf16, ids, w, T: int, k: int, y, ws=None,
