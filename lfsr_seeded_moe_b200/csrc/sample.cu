@@ -101,6 +101,7 @@ struct alignas(16) Shared {
   uint64_t slot[2][2][kMaxCluster];
   alignas(16) float group_max[kGroups];
   uint64_t warp_mass[kWarps];
+  uint32_t warp_count[kWarps];
   float warp_lo[kWarps], warp_hi[kWarps];
   float m, list_from;
   int32_t list_n;
@@ -113,13 +114,16 @@ struct alignas(16) Shared {
     struct {
       Candidate mine[kList], list[kList], sorted[kList];  // the CTA's part, and in CTA 0 all
       int32_t place[kList];                               // of the sorted, by their indexes
+      // by buckets
+      uint64_t key[kList];
+      uint32_t low[kList], start[kThreads + 1];
     };
   };
 };
 
-template <class T> __device__ __forceinline__ T warp_sum_of(T v) {
+template <int LANES = 32, class T> __device__ __forceinline__ T warp_sum_of(T v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 template <class T> __device__ __forceinline__ T warp_scan_of(T v, int lane) {  // inclusive
@@ -129,6 +133,72 @@ template <class T> __device__ __forceinline__ T warp_scan_of(T v, int lane) {  /
     if (lane >= o) v += y;
   }
   return v;
+}
+
+// Puts the n candidates of s.list in order, in s.sorted, with their places in
+// the order of their indexes.
+//
+// Up to 64: each one's place is the number of those before it, counted by 8
+// threads.  More: two bucket sorts at once, kThreads buckets by the logit
+// (from `top` down, 1 / scale each) and by the index (2^shift each), with the
+// two counts in the halves of a word; then each counts those of its buckets
+// that come before it, one or two unless logits are equal.  Of 55 candidates
+// the first takes 1050 cycles and the second 2600, of 177 they take 4700 and
+// 3400.
+__device__ __forceinline__ void sort_list(Shared &s, int n, float top, float scale, int shift) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (n <= kThreads / 8) {
+    const int c = tid / 8;
+    const uint64_t key = s.list[min(c, n - 1)].key;
+    int order = 0, place = 0;
+#pragma unroll 4
+    for (int j = tid & 7; j < n; j += 8) {
+      const uint64_t k = s.list[j].key;
+      order += k > key;
+      place += (uint32_t)k > (uint32_t)key;
+    }
+    order = warp_sum_of<8>(place << 16 | order);
+    if (c < n && (tid & 7) == 0) s.sorted[order & 0xffff] = s.list[c], s.place[order & 0xffff] = order >> 16;
+    __syncthreads();
+    return;
+  }
+  s.start[tid] = 0;
+  __syncthreads();
+  Candidate x{};
+  int by_logit = 0, by_index = 0;
+  uint32_t at = 0;
+  if (tid < n) {
+    x = s.list[tid];
+    by_logit = max(0, min(kThreads - 1, (int)((top - x.logit()) * scale)));
+    by_index = x.index() >> shift;
+    at = atomicAdd(&s.start[by_logit], 1u) & 0xffff;
+    at |= atomicAdd(&s.start[by_index], 0x10000u) & 0xffff0000u;
+  }
+  __syncthreads();
+  const uint32_t mine = s.start[tid];
+  uint32_t before = warp_scan_of(mine, lane) - mine;
+  if (lane == 31) s.warp_count[warp] = before + mine;
+  __syncthreads();
+  before += warp_sum_of<32>(lane < warp ? s.warp_count[lane] : 0u);
+  s.start[tid] = before;
+  if (tid == kThreads - 1) s.start[kThreads] = before + mine;
+  __syncthreads();
+  const uint32_t low = (uint32_t)x.key;  // falls with the index
+  if (tid < n) {
+    s.key[(s.start[by_logit] + at) & 0xffff] = x.key;
+    s.low[(s.start[by_index] + (at & 0xffff0000u)) >> 16] = low;
+  }
+  __syncthreads();
+  if (tid < n) {
+    const int logit0 = s.start[by_logit] & 0xffff, logit1 = s.start[by_logit + 1] & 0xffff;
+    const int index0 = s.start[by_index] >> 16, index1 = s.start[by_index + 1] >> 16;
+    int order = logit0, place = index0;
+    for (int j = logit0; j < logit1; ++j) order += s.key[j] > x.key;
+    for (int j = index0; j < index1; ++j) place += s.low[j] > low;
+    s.sorted[order] = x;
+    s.place[order] = place;
+  }
+  __syncthreads();
 }
 
 // The tokens between two logits, in the order of their logits.
@@ -176,6 +246,7 @@ template <class T, bool RES> struct Row {
   int rank, ctas;  // in the cluster
   int warp, lane;
   int parity = 0;
+  int index_shift = 0;    // of an index to one of kThreads buckets
   bool infinite = false;  // +inf occurs: those are 0, all others -inf
   Weight w{};
   // the last token that stays, in the order of descending logits and ascending indexes
@@ -413,26 +484,6 @@ template <class T, bool RES> struct Row {
     }
     return before;
   }
-  // Thread j gets the j-th of the list's n in their order.  Each candidate's
-  // place is the number of those before it, counted by up to 8 threads: 65536
-  // comparisons at most, of 4 instructions; sums in the same loop took 12.
-  __device__ __forceinline__ Candidate sorted(int n) {
-    const int per = n <= 64 ? 8 : n <= 128 ? 4 : 2, c = threadIdx.x / per;
-    const Candidate x = s.list[min(c, n - 1)];
-    int order = 0, place = 0;
-#pragma unroll 4
-    for (int j = threadIdx.x & (per - 1); j < n; j += per) {
-      const uint64_t key = s.list[j].key;
-      order += key > x.key;
-      place += (uint32_t)key > (uint32_t)x.key;
-    }
-    order |= place << 16;
-    for (int o = 1; o < per; o <<= 1) order += __shfl_xor_sync(0xffffffffu, order, o);
-    if (c < n && threadIdx.x % per == 0) s.sorted[order & 0xffff] = x, s.place[order & 0xffff] = order >> 16;
-    __syncthreads();
-    return s.sorted[min((int)threadIdx.x, n - 1)];
-  }
-
   // Sets the last token that stays to the one at which the kept tokens' count
   // (by_mass: their mass), in their order, first reaches `need`.  r: where it
   // is, from its top down to where weights are 0; kept tokens that are too few
@@ -463,14 +514,13 @@ template <class T, bool RES> struct Row {
       // reads run at once: one after another they took 17000 cycles)
       constexpr int kPer = kBins / kThreads;
       const int log = __ffs(ctas) - 1, b0 = (rank * kThreads + threadIdx.x) * kPer >> log;
-      uint64_t x[kPer], sum = 0;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
+      auto value = [&](int q) {
         const Shared *o = cg::this_cluster().map_shared_rank(&s, q & (ctas - 1));
-        x[q] = (uint64_t)o->hist.hi[b0 + (q >> log)] << 32 | o->hist.lo[b0 + (q >> log)];
-      }
+        return (uint64_t)o->hist.hi[b0 + (q >> log)] << 32 | o->hist.lo[b0 + (q >> log)];
+      };
+      uint64_t sum = 0;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) sum += x[q];
+      for (int q = 0; q < kPer; ++q) sum += value(q);
       uint64_t upto = warp_scan_of(sum, lane);
       if (lane == 31) s.warp_mass[warp] = upto;
       __syncthreads();
@@ -486,14 +536,11 @@ template <class T, bool RES> struct Row {
       for (int k = 0; k < warp; ++k) upto += s.warp_mass[k];
       if (threadIdx.x == 0) s.found = -1, s.list_n = 0;
       __syncthreads();
-      sum = 0;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        sum += x[q];
-        if ((q + 1) & (ctas - 1)) continue;  // the bin goes on
-        if (upto < need && need <= upto + sum) s.found = b0 + (q >> log), s.found_mass = upto;
-        upto += sum;
-        sum = 0;
+      if (upto < need && need <= upto + sum) {  // one thread: its bins again
+        for (int q = 0; q < kPer && upto < need;) {
+          s.found = b0 + (q >> log), s.found_mass = upto;
+          do upto += value(q); while (++q & (ctas - 1));
+        }
       }
       __syncthreads();
       const uint64_t mine[2] = {(uint64_t)(s.found + 1), s.found >= 0 ? s.found_mass : 0};
@@ -545,7 +592,9 @@ template <class T, bool RES> struct Row {
     const int len = gather(publish(count)[0]);
     uint64_t found[1] = {0};  // the token's key
     if (rank == 0 && len <= kList) {
-      const Candidate x = sorted(len);
+      const float top = fminf(r.top, r.hi);
+      sort_list(s, len, top, __fdividef(kThreads, top - r.lo), index_shift);
+      const Candidate x = s.sorted[min((int)threadIdx.x, len - 1)];
       const uint64_t w = threadIdx.x >= len ? 0 : by_mass ? x.w : 1;
       uint64_t all;
       const uint64_t before = r.above + sum_before(w, all);
@@ -624,6 +673,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
   }
   Row<T, RES> r{s, l, src, n, first, rank, ctas, tid >> 5, tid & 31};
+  static_assert(kThreads == 512);
+  r.index_shift = max(0, 32 - __clz(p.V - 1) - 9);
   if constexpr (!RES) r.template each<4>([&](int, float v) { hi = fmaxf(hi, v); });
 
   const float temp = p.temperature ? p.temperature[row] : 1.f;
@@ -722,7 +773,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     uint64_t good[2] = {0, 0}, need = 0, before = 0, Z;
     Candidate x{};
     if (rank == 0 && len <= kList) {
-      x = r.sorted(len);
+      // buckets down to 20 temperatures below m, if the list goes that far
+      sort_list(s, len, hi, __fdividef(kThreads, fminf(hi - from, 20.f * temp)), r.index_shift);
+      x = s.sorted[min(tid, len - 1)];
       before = r.sum_before(tid < len ? x.w : 0, Z);
       if (tid == (by_count ? min(top_k, len) : len) - 1) s.found_mass = before + x.w;
       if (tid == len - 1) s.found = r.w(x.logit()) < min_w || p.V <= kList;
