@@ -106,8 +106,8 @@ template <int BYTES> __device__ __forceinline__ void copy(uint32_t dst, const vo
 template <int G> constexpr int kGroups = kStageK / G;             // of a stage: 8, 4 or 2
 // Scales are copied 8 groups (16 bytes) of a row at once where whole rows and
 // the warps' ranges allow it and there are rows enough for it to matter: each
-// row's piece is a transaction of its own, whatever its size.  (8192 weights of
-// 64-weight groups by 8-byte copies: 80 us at 131072 x 4096, by 16-byte ones 66.)
+// row's piece is a transaction of its own, whatever its size.  (Groups of 64 by
+// 8-byte copies: 80 us at 131072 x 4096 and 8 vectors, by 16-byte ones 66.)
 constexpr int kScaleRow = 16;
 constexpr int kScales = kTile * kScaleRow;
 template <bool AFFINE> constexpr int kSlot = kStage + kScales * (AFFINE ? 2 : 1);

@@ -17,9 +17,13 @@ constexpr int kMaxV = 1 << 18;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 4096;
-constexpr int kList = 256;
-constexpr int kGroups = 128;  // parts of a row whose largest logits are known
-constexpr int kListAt = 96;   // and the one of those, in descending order, from which on a list is made for top-p
+constexpr int kList = 2 * kThreads;  // candidates that are sorted
+constexpr int kFew = kThreads / 8;    // up to here they are compared with one another
+constexpr int kAll = 256;            // a row of so few logits is one list
+constexpr int kGroups = 128;         // parts of a row whose largest logits are known
+constexpr int kListAt = 96;          // and the one of those, in descending order, that has a list of the first top_k at most
+constexpr int kListMass = 96;        // and the one from which on a list is made for top-p
+constexpr int kCountBins = 2 * kThreads;
 
 struct SampleParams {
   const void *logits;
@@ -80,20 +84,16 @@ struct Weight {
 };
 
 // A token of a list: its logit in the order of its values, then its index
-// falling, so that of two the larger comes first; and its weight.
-struct alignas(16) Candidate {
-  uint64_t key, w;
-
-  static __device__ __forceinline__ Candidate of(float v, int i, uint64_t w) {
-    const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
-    return Candidate{(uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | ~(uint32_t)i, w};
-  }
-  __device__ __forceinline__ int index() const { return (int)~(uint32_t)key; }
-  __device__ __forceinline__ float logit() const {
-    const uint32_t k = (uint32_t)(key >> 32);
-    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-  }
-};
+// falling, so that of two the larger comes first.
+__device__ __forceinline__ uint64_t key_of(float v, int i) {
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
+  return (uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | ~(uint32_t)i;
+}
+__device__ __forceinline__ int index_of(uint64_t key) { return (int)~(uint32_t)key; }
+__device__ __forceinline__ float logit_of(uint64_t key) {
+  const uint32_t k = (uint32_t)(key >> 32);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
 
 struct alignas(16) Shared {
   double pow16[16];
@@ -103,7 +103,7 @@ struct alignas(16) Shared {
   uint64_t warp_mass[kWarps];
   uint32_t warp_count[kWarps];
   float warp_lo[kWarps], warp_hi[kWarps];
-  float m, list_from;
+  float m, list_from, list_top;
   int32_t list_n;
   int32_t found;
   uint64_t found_mass;
@@ -112,10 +112,18 @@ struct alignas(16) Shared {
       uint32_t lo[kBins], hi[kBins];
     } hist;
     struct {
-      Candidate mine[kList], list[kList], sorted[kList];  // the CTA's part, and in CTA 0 all
-      int32_t place[kList];                               // of the sorted, by their indexes
-      // by buckets
-      uint64_t key[kList];
+      uint64_t mine[kList];            // the CTA's part of a list; in CTA 0 then the whole in order, then by indexes
+      union {
+        uint64_t list[kList];          // in CTA 0 all parts
+        struct {
+          uint64_t few[kFew];          // (what a short list needs while `place` is written)
+          uint16_t place[kList];       // of the sorted, by their indexes
+        };
+      };
+      union {
+        uint64_t key[kList];           // while they are sorted; then the weights by their indexes
+        uint32_t count[kCountBins];    // before there is a list
+      };
       uint32_t low[kList], start[kThreads + 1];
     };
   };
@@ -135,70 +143,180 @@ template <class T> __device__ __forceinline__ T warp_scan_of(T v, int lane) {  /
   return v;
 }
 
-// Puts the n candidates of s.list in order, in s.sorted, with their places in
-// the order of their indexes.
+// Puts the n candidates of s.list in order, in s.mine, with their places in the
+// order of their indexes.
 //
 // Up to 64: each one's place is the number of those before it, counted by 8
 // threads.  More: two bucket sorts at once, kThreads buckets by the logit
 // (from `top` down, 1 / scale each) and by the index (2^shift each), with the
 // two counts in the halves of a word; then each counts those of its buckets
-// that come before it, one or two unless logits are equal.  Of 55 candidates
+// that come before it, a few unless logits are equal.  (What is above `top` has
+// the first bucket: a few again, and one far outlier stretches none.)  Of 55 candidates
 // the first takes 1050 cycles and the second 2600, of 177 they take 4700 and
 // 3400.
 __device__ __forceinline__ void sort_list(Shared &s, int n, float top, float scale, int shift) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (n <= kThreads / 8) {
+  if (n <= kFew) {
     const int c = tid / 8;
-    const uint64_t key = s.list[min(c, n - 1)].key;
+    const uint64_t key = s.list[min(c, n - 1)];
     int order = 0, place = 0;
 #pragma unroll 4
     for (int j = tid & 7; j < n; j += 8) {
-      const uint64_t k = s.list[j].key;
+      const uint64_t k = s.list[j];
       order += k > key;
       place += (uint32_t)k > (uint32_t)key;
     }
     order = warp_sum_of<8>(place << 16 | order);
-    if (c < n && (tid & 7) == 0) s.sorted[order & 0xffff] = s.list[c], s.place[order & 0xffff] = order >> 16;
+    if (c < n && (tid & 7) == 0) s.mine[order & 0xffff] = key, s.place[order & 0xffff] = (uint16_t)(order >> 16);
     __syncthreads();
     return;
   }
+  constexpr int kPer = kList / kThreads;
   s.start[tid] = 0;
   __syncthreads();
-  Candidate x{};
-  int by_logit = 0, by_index = 0;
-  uint32_t at = 0;
-  if (tid < n) {
-    x = s.list[tid];
-    by_logit = max(0, min(kThreads - 1, (int)((top - x.logit()) * scale)));
-    by_index = x.index() >> shift;
-    at = atomicAdd(&s.start[by_logit], 1u) & 0xffff;
-    at |= atomicAdd(&s.start[by_index], 0x10000u) & 0xffff0000u;
+  uint64_t x[kPer];
+  int by_logit[kPer], by_index[kPer];
+  uint32_t at[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    if (tid + q * kThreads >= n) break;
+    x[q] = s.list[tid + q * kThreads];
+    by_logit[q] = max(0, min(kThreads - 1, (int)((top - logit_of(x[q])) * scale)));
+    by_index[q] = index_of(x[q]) >> shift;
+    at[q] = atomicAdd(&s.start[by_logit[q]], 1u) & 0xffff;
+    at[q] |= atomicAdd(&s.start[by_index[q]], 0x10000u) & 0xffff0000u;
   }
   __syncthreads();
   const uint32_t mine = s.start[tid];
   uint32_t before = warp_scan_of(mine, lane) - mine;
   if (lane == 31) s.warp_count[warp] = before + mine;
   __syncthreads();
-  before += warp_sum_of<32>(lane < warp ? s.warp_count[lane] : 0u);
+  before += warp_sum_of(lane < warp ? s.warp_count[lane] : 0u);
   s.start[tid] = before;
   if (tid == kThreads - 1) s.start[kThreads] = before + mine;
   __syncthreads();
-  const uint32_t low = (uint32_t)x.key;  // falls with the index
-  if (tid < n) {
-    s.key[(s.start[by_logit] + at) & 0xffff] = x.key;
-    s.low[(s.start[by_index] + (at & 0xffff0000u)) >> 16] = low;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    if (tid + q * kThreads >= n) break;
+    s.key[(s.start[by_logit[q]] + at[q]) & 0xffff] = x[q];
+    s.low[(s.start[by_index[q]] + (at[q] & 0xffff0000u)) >> 16] = (uint32_t)x[q];
   }
   __syncthreads();
-  if (tid < n) {
-    const int logit0 = s.start[by_logit] & 0xffff, logit1 = s.start[by_logit + 1] & 0xffff;
-    const int index0 = s.start[by_index] >> 16, index1 = s.start[by_index + 1] >> 16;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    if (tid + q * kThreads >= n) break;
+    const int logit0 = s.start[by_logit[q]] & 0xffff, logit1 = s.start[by_logit[q] + 1] & 0xffff;
+    const int index0 = s.start[by_index[q]] >> 16, index1 = s.start[by_index[q] + 1] >> 16;
     int order = logit0, place = index0;
-    for (int j = logit0; j < logit1; ++j) order += s.key[j] > x.key;
-    for (int j = index0; j < index1; ++j) place += s.low[j] > low;
-    s.sorted[order] = x;
-    s.place[order] = place;
+    for (int j = logit0; j < logit1; ++j) order += s.key[j] > x[q];
+    for (int j = index0; j < index1; ++j) place += s.low[j] > (uint32_t)x[q];  // these fall with the index
+    s.mine[order] = x[q];
+    s.place[order] = (uint16_t)place;
   }
   __syncthreads();
+}
+
+// The sum of the CTA's values before this thread's, and of all.
+__device__ __forceinline__ uint64_t sum_before(Shared &s, uint64_t v, uint64_t &all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t upto = warp_scan_of(v, lane);
+  __syncthreads();
+  if (lane == 31) s.warp_mass[warp] = upto;
+  __syncthreads();
+  uint64_t before = upto - v;
+  all = 0;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) {
+    const uint64_t x = s.warp_mass[k];
+    before += k < warp ? x : 0;
+    all += x;
+  }
+  return before;
+}
+
+// The candidate of s.list at which the count or mass in their order first
+// reaches `need`: its key to s.found_mass.
+__device__ __forceinline__ void find_in_list(Shared &s, int n, float top, float scale, int shift, uint64_t need, bool by_mass,
+                                          Weight w) {
+  sort_list(s, n, top, scale, shift);
+  const int at = 2 * threadIdx.x;  // of two each thread has
+  uint64_t x[2], m[2], all;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    x[q] = at + q < n ? s.mine[at + q] : 0;
+    m[q] = at + q >= n ? 0 : by_mass ? w.fixed(logit_of(x[q])) : 1;
+  }
+  uint64_t before = sum_before(s, m[0] + m[1], all);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (before < need && need <= before + m[q]) s.found_mass = x[q];
+    before += m[q];
+  }
+  __syncthreads();
+}
+
+// Of a row whose kept tokens weigh `all`, the weight that the token's sum exceeds.
+__device__ __forceinline__ uint64_t target_of(float u, uint64_t all) {
+  if (!(u > 0.f)) return 0;
+  return u < 1.f ? min((uint64_t)((double)u * (double)all), all - 1) : all - 1;
+}
+// The least mass that top-p keeps.
+__device__ __forceinline__ uint64_t need_of(float top_p, uint64_t all) {
+  return (uint64_t)max(__double2ll_ru((double)top_p * (double)all), 1ll);
+}
+
+struct ListTask {
+  Weight weight;
+  double min_w;
+  uint64_t all;      // the row's mass, if top-p asks for it
+  float top, scale;  // of the sort's buckets
+  float u, top_p;
+  int top_k;         // 0: off
+  bool by_mass;
+  int n, shift;
+};
+
+// Draws the row's token from the n candidates of s.list, if all that stay are
+// among them; else false.  Their mass, or top-k's, in s.found_mass.
+__device__ __forceinline__ bool draw_from_list(Shared &s, const SampleParams &p, int row, ListTask t) {
+  const int tid = threadIdx.x, at = 2 * tid;  // of two tokens each thread has
+  sort_list(s, t.n, t.top, t.scale, t.shift);
+  const int limit = t.top_k ? min(t.top_k, t.n) : t.n;
+  uint64_t x[2], m[2], Z;
+  bool stays[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    x[q] = at + q < t.n ? s.mine[at + q] : 0;
+    const double w = at + q < t.n ? t.weight(logit_of(x[q])) : 0.;
+    stays[q] = at + q < limit && (at + q == 0 || w >= t.min_w);
+    m[q] = Weight::to_fixed(w);
+    if (at + q == t.n - 1) s.found = w < t.min_w || p.V <= kAll;
+  }
+  const uint64_t before = sum_before(s, m[0] + m[1], Z);
+  if (at == limit - 1) s.found_mass = before + m[0];
+  if (at + 1 == limit - 1) s.found_mass = before + m[0] + m[1];
+  __syncthreads();
+  // all that stays is in the list if its end is behind top-k's, top-p's or min-p's
+  const uint64_t need = t.by_mass ? need_of(t.top_p, t.top_k ? s.found_mass : t.all) : s.found_mass + 1;
+  if (t.top_k ? !(t.n >= t.top_k || (s.found && (!t.by_mass || p.V <= kAll))) : !(s.found || s.found_mass >= need)) return false;
+  // of the first top_k, those stay with less than need before them that min-p leaves; then all by their indexes
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (at + q >= t.n) break;
+    const int place = s.place[at + q];
+    s.mine[place] = x[q];
+    s.key[place] = stays[q] && before + (q ? m[0] : 0) < need ? m[q] : 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) m[q] = at + q < t.n ? s.key[at + q] : 0;
+  const uint64_t below = sum_before(s, m[0] + m[1], Z), to = target_of(t.u, Z);
+  if (below <= to && to < below + m[0] + m[1]) {
+    const uint64_t y = s.mine[at + (to < below + m[0] ? 0 : 1)];
+    p.token[row] = index_of(y);
+    if (p.prob) p.prob[row] = (float)(t.weight(logit_of(y)) / (double)Z);
+  }
+  return true;
 }
 
 // The tokens between two logits, in the order of their logits.
@@ -235,7 +353,7 @@ struct Range {
 __device__ __forceinline__ float logit_of(float v) { return fmaxf(v, -INFINITY); }
 __device__ __forceinline__ float logit_of(__nv_bfloat16 v) { return logit_of(__bfloat162float(v)); }
 
-constexpr int kRing = 4, kRingChunk = 1024;  // chunks of a warp's ring, and their bytes
+constexpr int kRing = 4, kRingChunk = 512;  // chunks of a warp's ring, and their bytes
 
 template <class T, bool RES> struct Row {
   Shared &s;
@@ -451,7 +569,7 @@ template <class T, bool RES> struct Row {
   // last barrier; what is behind its end is counted only.
   __device__ __forceinline__ void add_to_list(int i, float v) const {
     const int at = atomicAdd(&s.list_n, 1);
-    if (at < kList) s.mine[at] = Candidate::of(v, first + i, w.fixed(v));
+    if (at < kList) s.mine[at] = key_of(v, first + i);
   }
   // The parts of all CTAs, of `counts` tokens, together in CTA 0: their number,
   // and the list if it has room for them.
@@ -459,30 +577,14 @@ template <class T, bool RES> struct Row {
     int total = 0;
     for (int k = 0; k < ctas; ++k) total += (int)counts[k];
     if (rank != 0 || total > kList) return total;
-    int c = threadIdx.x, k = 0;
-    if (c < total) {
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+      int c = i, k = 0;
       while (c >= (int)counts[k]) c -= (int)counts[k++];
       const Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, k);
-      s.list[threadIdx.x] = o->mine[c];
+      s.list[i] = o->mine[c];
     }
     __syncthreads();
     return total;
-  }
-  // The sum of the threads' values before this one's, and of all.
-  __device__ __forceinline__ uint64_t sum_before(uint64_t v, uint64_t &all) const {
-    const uint64_t upto = warp_scan_of(v, lane);
-    __syncthreads();
-    if (lane == 31) s.warp_mass[warp] = upto;
-    __syncthreads();
-    uint64_t before = upto - v;
-    all = 0;
-#pragma unroll
-    for (int k = 0; k < kList / 32; ++k) {  // only those threads have any
-      const uint64_t x = s.warp_mass[k];
-      before += k < warp ? x : 0;
-      all += x;
-    }
-    return before;
   }
   // Sets the last token that stays to the one at which the kept tokens' count
   // (by_mass: their mass), in their order, first reaches `need`.  r: where it
@@ -593,20 +695,13 @@ template <class T, bool RES> struct Row {
     uint64_t found[1] = {0};  // the token's key
     if (rank == 0 && len <= kList) {
       const float top = fminf(r.top, r.hi);
-      sort_list(s, len, top, __fdividef(kThreads, top - r.lo), index_shift);
-      const Candidate x = s.sorted[min((int)threadIdx.x, len - 1)];
-      const uint64_t w = threadIdx.x >= len ? 0 : by_mass ? x.w : 1;
-      uint64_t all;
-      const uint64_t before = r.above + sum_before(w, all);
-      if (before < need && need <= before + w) s.found_mass = x.key;
-      __syncthreads();
+      find_in_list(s, len, top, __fdividef(kThreads, top - r.lo), index_shift, need - r.above, by_mass, w);
       found[0] = s.found_mass;
     }
     const auto slot = publish(found);
     if (!slot[0][0]) return false;
-    const Candidate last{slot[0][0], 0};
-    last_v = last.logit();
-    last_i = last.index();
+    last_v = logit_of(slot[0][0]);
+    last_i = index_of(slot[0][0]);
     return true;
   }
 };
@@ -622,8 +717,38 @@ template <class T, bool RES> __device__ __noinline__ Last cut_row(Row<T, RES> r,
   return Last{r.last_v, r.last_i, r.parity};
 }
 
+// A list of the first top_k tokens, which reach below `from`, has to begin
+// lower: at the bin of a histogram of 8 temperatures below that has the k-th,
+// and a little lower yet for its rounding.
+template <class T, bool RES> __device__ __noinline__ float list_start(Row<T, RES> r, float from, int top_k, float temp) {
+  const int tid = threadIdx.x;
+  const float scale = __fdividef(kCountBins, 8.f * temp);
+  r.template each<4>([&](int, float v) {
+    const int b = (int)((from - v) * scale);
+    if (b < kCountBins) atomicAdd(&r.s.count[max(0, b)], 1u);
+  });
+  if (tid == 0) r.s.found = -1;
+  r.sync_row();
+  // every CTA adds all histograms: two bins a thread
+  uint2 mine = make_uint2(0, 0);
+#pragma unroll
+  for (int k = 0; k < kMaxCluster; ++k) {
+    if (k >= r.ctas) break;
+    const uint2 x = reinterpret_cast<const uint2 *>(cg::this_cluster().map_shared_rank(r.s.count, k))[tid];
+    mine.x += x.x, mine.y += x.y;
+  }
+  int upto = warp_scan_of((int)(mine.x + mine.y), r.lane);
+  if (r.lane == 31) r.s.warp_count[r.warp] = upto;
+  __syncthreads();
+  upto += (int)warp_sum_of(r.lane < r.warp ? r.s.warp_count[r.lane] : 0u);
+  if (upto - (int)(mine.x + mine.y) < top_k && top_k <= upto) r.s.found = 2 * tid + (upto - (int)mine.y < top_k ? 1 : 0);
+  __syncthreads();
+  const int bin = r.s.found;
+  return bin < 0 ? from : fmaxf(from - __fdividef(bin + 1.25f, scale), -FLT_MAX);
+}
+
 template <class T, bool RES>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ float4 smem[];
   Shared &s = *reinterpret_cast<Shared *>(smem);
   cg::cluster_group cluster = cg::this_cluster();
@@ -647,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       hi = fmaxf(hi, v);
       return v;
     };
-    const int vecs = (n - head) / kVec;
+    // every thread has a part in a row's maxima: of a short part it takes single logits
+    const int vecs = n < kThreads * kVec ? 0 : (n - head) / kVec;
 #pragma unroll 4
     for (int i = tid; i < vecs; i += kThreads) {
       const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(src + head) + i);
@@ -667,10 +793,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       for (int j = 0; j < kVec; j += 4) dst[j / 4] = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
     }
     if (tid < head) l[tid] = put(logit_of(src[tid]));
-    if (tid < n - head - vecs * kVec) {
-      const int i = head + vecs * kVec + tid;
-      l[i] = put(logit_of(src[i]));
-    }
+#pragma unroll 4
+    for (int i = head + vecs * kVec + tid; i < n; i += kThreads) l[i] = put(logit_of(src[i]));
   }
   Row<T, RES> r{s, l, src, n, first, rank, ctas, tid >> 5, tid & 31};
   static_assert(kThreads == 512);
@@ -690,11 +814,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     to[rank * (kGroups / ctas) + tid / width] = hi;
   }
   if (tid == 0) s.list_n = 0;
+  s.count[tid] = s.count[tid + kThreads] = 0;
   r.sync_row();
   // k of them reach the k-th, so k tokens do, and seldom many more: a list from
   // there on has a top-k, and of most rows a top-p
   if (by_count || by_mass) {
-    const int at = by_count ? min(top_k, kListAt) : kListAt;
+    const int at = by_count ? min(top_k, kListAt) : kListMass;
     constexpr int kShare = kThreads / kGroups;  // neighbouring threads share a part's comparisons
     const int c = tid / kShare;
     const float x = s.group_max[c];
@@ -712,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     for (int o = 1; o < kShare; o <<= 1) order += __shfl_xor_sync(0xffffffffu, order, o);
     if (order == 0) s.m = x;
     if (order == at - 1) s.list_from = x;
+    if (order == min(at, 8) - 1) s.list_top = x;
     __syncthreads();
     hi = s.m;
   } else {
@@ -738,18 +864,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   }
   r.w = Weight{hi, fmaxf(__fmaf_rn(-40.f, temp, hi), -FLT_MAX), 16. / (0.69314718055994530942 * (double)temp), s.pow16};
   const double min_w = q > 0.f ? fmin((double)q, 1.) * 0x1p44 : 0.;
-  auto target = [&](uint64_t all) -> uint64_t {
-    if (greedy || !(u > 0.f)) return 0;
-    return u < 1.f ? min((uint64_t)((double)u * (double)all), all - 1) : all - 1;
-  };
-  auto need_of = [&](uint64_t all) -> uint64_t {
-    return (uint64_t)max(__double2ll_ru((double)top_p * (double)all), 1ll);
-  };
+  auto target = [&](uint64_t all) -> uint64_t { return greedy ? 0 : target_of(u, all); };
 
   uint64_t all_mass = 0, list_mass = 0;  // of the row, and from list_from on
   float list_from = INFINITY;
   if (by_count || by_mass) {
-    const float from = p.V <= kList || r.infinite ? -FLT_MAX : fmaxf(s.list_from, -FLT_MAX);
+    float from = p.V <= kAll || r.infinite ? -FLT_MAX : fmaxf(s.list_from, -FLT_MAX);
+    if (by_count && top_k > kListAt && top_k <= kList && from > -FLT_MAX) from = list_start(r, from, top_k, temp);
     uint64_t sum[2] = {0, 0};
     if (by_count) {
       r.template each<4>([&](int i, float v) {
@@ -769,38 +890,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const auto slot = r.publish(sum);
     const int len = r.gather(slot[1]);
     for (int k = 0; k < ctas; ++k) all_mass += slot[0][k];
-    // CTA 0 puts the list in order: a token's place, and the mass before it
-    uint64_t good[2] = {0, 0}, need = 0, before = 0, Z;
-    Candidate x{};
+    // CTA 0 tells the others whether the list had the token
+    uint64_t good[2] = {0, 0};
     if (rank == 0 && len <= kList) {
-      // buckets down to 20 temperatures below m, if the list goes that far
-      sort_list(s, len, hi, __fdividef(kThreads, fminf(hi - from, 20.f * temp)), r.index_shift);
-      x = s.sorted[min(tid, len - 1)];
-      before = r.sum_before(tid < len ? x.w : 0, Z);
-      if (tid == (by_count ? min(top_k, len) : len) - 1) s.found_mass = before + x.w;
-      if (tid == len - 1) s.found = r.w(x.logit()) < min_w || p.V <= kList;
-      __syncthreads();
-      // all that stays is in the list if its end is behind top-k's, top-p's or min-p's
-      const bool whole = s.found || (by_count && len >= top_k);
-      need = by_mass ? need_of(by_count ? s.found_mass : all_mass) : s.found_mass + 1;
-      good[0] = by_count ? whole && (!by_mass || len >= top_k || p.V <= kList) : whole || s.found_mass >= need;
+      // buckets down to the list's end; of a whole row to 40 temperatures, below which weights are 0
+      const float top = r.infinite ? hi : s.list_top;
+      const float scale = __fdividef(kThreads, from > -FLT_MAX ? top - from : 40.f * temp);
+      good[0] = draw_from_list(s, p, row, ListTask{r.w, min_w, all_mass, top, scale, u, top_p, by_count ? top_k : 0, by_mass, len, r.index_shift});
       good[1] = s.found_mass;
     }
     const auto told = r.publish(good);
     list_from = told[1][0] && !by_count ? from : INFINITY;
     list_mass = told[1][0];
-    if (told[0][0]) {
-      if (rank != 0) return;
-      // tokens that stay: of the first top_k, those with less than need before them that min-p leaves;
-      // then all by their indexes
-      const bool stays = tid < (by_count ? min(top_k, len) : len) && before < need && (tid == 0 || r.w(x.logit()) >= min_w);
-      if (tid < len) s.list[s.place[tid]] = Candidate{x.key, stays ? x.w : 0};
-      __syncthreads();
-      if (tid < len) x = s.list[tid];
-      const uint64_t w = tid < len ? x.w : 0, below = r.sum_before(w, Z), at = target(Z);
-      if (below <= at && at < below + w) put_out(x.index(), (float)(r.w(x.logit()) / (double)Z));
-      return;
-    }
+    if (told[0][0]) return;
   }
   if (by_count || by_mass) {
     // the slow way: down to 32 temperatures below m, where weights are 0
@@ -833,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       range.lo = fminf(range.lo, list_from);
       range.above = list_mass;
     }
-    if (by_mass) cut(need_of(all_mass), true);
+    if (by_mass) cut(need_of(top_p, all_mass), true);
   }
   uint64_t Z;
   int at;

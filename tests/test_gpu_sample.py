@@ -333,3 +333,21 @@ def test_two_calls_at_once(nslm):
     torch.cuda.synchronize()
     for i in range(2):
         assert np.array_equal(out[i].cpu().numpy(), _want(l, u[i], top_p=p)[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V", [(6, 300), (6, 1025), (6, 5003), (6, 40000), (100, 20011)])
+def test_lists_of_hundreds(nslm, B, V, dtype):
+    # top-k from tens to past a thousand, over rows of one far outlier, of few values, and nearly even ones,
+    # from cold to hot
+    l = _logits(B, V, V + 1, 2.0, dtype)
+    l[1::6, V // 3] = 900.0
+    l[2::6] = (2 * l[2::6].float()).round().to(dtype) / 2
+    l[3::6] *= 0.01
+    l[4::6, : V // 2] = -float("inf")
+    u = torch.rand(B, generator=_gen(V), device="cuda")
+    for k in (60, 97, 250, 500, 1000, 1024, 1025):
+        ks = _full(B, k, torch.int32)
+        for t in (0.05, 1.0, 5.0):
+            _check(nslm, l, u, t=_full(B, t), top_k=ks)
+        _check(nslm, l, u, top_k=ks, top_p=_full(B, 0.95), min_p=_full(B, 0.001))
