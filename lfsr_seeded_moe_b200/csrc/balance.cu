@@ -322,9 +322,10 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(const BalanceP
 // dlogits may be logits: a token's lanes have read it before they write it.
 constexpr int kGradThreads = 128;
 
-template <class Tok> __global__ void __launch_bounds__(kGradThreads) balance_grad_kernel(const float *logits, const int32_t *counts, const uint8_t *mask,
-                                                                                         int T, int E, int k, float coef,
-                                                                                         const float *dloss, float *dlogits) {
+template <class Tok>
+__global__ void __launch_bounds__(kGradThreads)
+    balance_grad_kernel(const float *logits, const int32_t *counts, const uint8_t *mask, int T, int E, int k, float coef,
+                        const float *dloss, float *dlogits) {
   __shared__ int32_t s_total[kGradThreads / 32];
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -439,7 +440,8 @@ extern "C" int32_t nslm_moe_balance(const float *logits, const int32_t *ids, con
   BalanceParams p{logits, ids, mask, T, E, k, coef, counts, offsets, mean_p, loss, nullptr, nullptr, 0};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (T <= kOneLaunchT) {
-    // a cluster's barriers cost about what 64 tokens do, and a CTA has a thread for each column of its slice and one more in the end
+    // a cluster's barriers cost about what 64 tokens do; and in the end a CTA has
+    // a thread for each column of its slice and one more
     int ctas = 1;
     while (ctas < kCluster && (T > 64 * ctas || ceil_div(E, ctas) + 1 > kThreads)) ctas *= 2;
     st = with_token(E, [&](auto tok) {

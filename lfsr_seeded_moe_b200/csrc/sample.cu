@@ -17,13 +17,16 @@ constexpr int kMaxV = 1 << 18;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 4096;
-constexpr int kList = 2 * kThreads;  // candidates that are sorted
-constexpr int kFew = kThreads / 8;    // up to here they are compared with one another
-constexpr int kAll = 256;            // a row of so few logits is one list
-constexpr int kGroups = 128;         // parts of a row whose largest logits are known
-constexpr int kListAt = 96;          // and the one of those, in descending order, that has a list of the first top_k at most
-constexpr int kListMass = 96;        // and the one from which on a list is made for top-p
-constexpr int kCountBins = 2 * kThreads;
+constexpr int kList = 2 * kThreads;       // candidates that are sorted
+constexpr int kFew = kThreads / 8;        // up to here they are compared with one another
+constexpr int kAll = 256;                 // a row of so few logits is one list
+constexpr int kCountBins = 2 * kThreads;  // that find where a long list begins
+constexpr int kGroups = 128;              // parts of a row whose largest logits are known
+constexpr int kListAt = 96;               // the last of those, in descending order, from which a top-k's list begins
+// The one from which on a list is made for top-p: 266 tokens on average.  At 96
+// (177) it costs 1 to 3% less, at 120 (355) as much more; a row whose top-p is
+// past its list costs 20 us and more.
+constexpr int kListMass = 112;
 
 struct SampleParams {
   const void *logits;
@@ -42,10 +45,15 @@ struct SampleParams {
 // fp32 (RES).  Of a larger batch it takes a longer part, which passes through
 // small rings of its warps each time it is needed, from the L2 after the first:
 // then a row's barriers, about 1 us each, are shared by more logits, and the
-// whole batch runs at once.  w is 64-bit fixed point with 44 bits
-// behind the point, at most 2^18 of them, so sums stay below 2^62 and are
-// exact: whatever order threads and CTAs add in, the same u gives the same
-// token.
+// whole batch runs at once (64 x 131072 with top-k 50: 34 us kept, 24 streamed).
+//
+// w is 64-bit fixed point with 44 bits behind the point, at most 2^18 of them,
+// so sums stay below 2^62 and are exact: whatever order threads and CTAs add in,
+// the same u gives the same token.
+//
+// One row of 32003 logits with top-k 50 and top-p takes 8.7 us, nearly all of it
+// the cluster's barriers; 64 x 131072 without a filter 31 us, bound by the
+// instructions of two passes (0.62 of the issue slots, DRAM at 15%).
 
 // Weights in units of 2^-44.  exp(x) = 2^(k/16) e^r, |r| <= ln 2 / 32, with the
 // 16 powers from a table and e^r by its series to r^5 (the table method of
@@ -146,7 +154,7 @@ template <class T> __device__ __forceinline__ T warp_scan_of(T v, int lane) {  /
 // Puts the n candidates of s.list in order, in s.mine, with their places in the
 // order of their indexes.
 //
-// Up to 64: each one's place is the number of those before it, counted by 8
+// Up to kFew: each one's place is the number of those before it, counted by 8
 // threads.  More: two bucket sorts at once, kThreads buckets by the logit
 // (from `top` down, 1 / scale each) and by the index (2^shift each), with the
 // two counts in the halves of a word; then each counts those of its buckets
@@ -896,7 +904,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       // buckets down to the list's end; of a whole row to 40 temperatures, below which weights are 0
       const float top = r.infinite ? hi : s.list_top;
       const float scale = __fdividef(kThreads, from > -FLT_MAX ? top - from : 40.f * temp);
-      good[0] = draw_from_list(s, p, row, ListTask{r.w, min_w, all_mass, top, scale, u, top_p, by_count ? top_k : 0, by_mass, len, r.index_shift});
+      good[0] = draw_from_list(s, p, row, ListTask{r.w, min_w, all_mass, top, scale, u, top_p, by_count ? top_k : 0, by_mass,
+                                                   len, r.index_shift});
       good[1] = s.found_mass;
     }
     const auto told = r.publish(good);
