@@ -94,6 +94,12 @@ template <int LANES, int NV, bool VEC> struct Token {
   }
 };
 
+// One pass over the logits with the running sums in registers.  65536 tokens of
+// 128 experts take 13.3 us in two launches, 3 of them the second and its wait;
+// the logits' 32 MB take 4.9 at the copy rate, and the exponentials, shuffles
+// and the ids' shared-memory atomics are the rest.  64 tokens of 100 experts
+// take 4.1 us, all latency.
+//
 // The CTA's tokens of a grid of `ctas`: the probabilities' sums to s_p[E], the
 // counts and the number of tokens to s_c[E + 1].  s_w: a row of E for each warp.
 template <class Tok, int THREADS>
@@ -317,7 +323,9 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(const BalanceP
       [&](int g, int e) { return p.part_c[(size_t)g * (p.E + 1) + e]; });
 }
 
-// f_e less its mean: a softmax's gradient does not see a constant, and a
+// The gradient: a pass that reads and writes each logit once, with the next
+// token's on their way: 65536 x 128 takes 12.8 us, 76% of the copy rate.
+// f is f_e less its mean: a softmax's gradient does not see a constant, and a
 // difference of two nearly equal sums would lose what f's differences hold.
 // dlogits may be logits: a token's lanes have read it before they write it.
 constexpr int kGradThreads = 128;
