@@ -224,23 +224,29 @@ __device__ __forceinline__ void sort_list(Shared &s, int n, float top, float sca
   __syncthreads();
 }
 
-// The sum of the CTA's values before this thread's, and of all.
-__device__ __forceinline__ uint64_t sum_before(Shared &s, uint64_t v, uint64_t &all) {
+// The sum of the values before this thread's, and of all, in the first `warps`
+// warps; the others have none and only wait.
+__device__ __forceinline__ uint64_t sum_before(Shared &s, uint64_t v, int warps, uint64_t &all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint64_t upto = warp_scan_of(v, lane);
-  __syncthreads();
-  if (lane == 31) s.warp_mass[warp] = upto;
-  __syncthreads();
-  uint64_t before = upto - v;
+  uint64_t before = 0;
   all = 0;
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    const uint64_t x = s.warp_mass[k];
-    before += k < warp ? x : 0;
-    all += x;
+  if (warp < warps) {
+    const uint64_t upto = warp_scan_of(v, lane);
+    if (lane == 31) s.warp_mass[warp] = upto;
+    before = upto - v;
+  }
+  __syncthreads();
+  if (warp < warps) {
+    for (int k = 0; k < warps; ++k) {
+      const uint64_t x = s.warp_mass[k];
+      before += k < warp ? x : 0;
+      all += x;
+    }
   }
   return before;
 }
+// The warps that have n candidates, two a thread.
+__device__ __forceinline__ int warps_of(int n) { return (n + 63) / 64; }
 
 // The candidate of s.list at which the count or mass in their order first
 // reaches `need`: its key to s.found_mass.
@@ -248,13 +254,14 @@ __device__ __forceinline__ void find_in_list(Shared &s, int n, float top, float 
                                           Weight w) {
   sort_list(s, n, top, scale, shift);
   const int at = 2 * threadIdx.x;  // of two each thread has
-  uint64_t x[2], m[2], all;
+  uint64_t x[2] = {0, 0}, m[2] = {0, 0}, all;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    x[q] = at + q < n ? s.mine[at + q] : 0;
-    m[q] = at + q >= n ? 0 : by_mass ? w.fixed(logit_of(x[q])) : 1;
+    if (at + q >= n) break;
+    x[q] = s.mine[at + q];
+    m[q] = by_mass ? w.fixed(logit_of(x[q])) : 1;
   }
-  uint64_t before = sum_before(s, m[0] + m[1], all);
+  uint64_t before = sum_before(s, m[0] + m[1], warps_of(n), all);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     if (before < need && need <= before + m[q]) s.found_mass = x[q];
@@ -289,18 +296,19 @@ struct ListTask {
 __device__ __forceinline__ bool draw_from_list(Shared &s, const SampleParams &p, int row, ListTask t) {
   const int tid = threadIdx.x, at = 2 * tid;  // of two tokens each thread has
   sort_list(s, t.n, t.top, t.scale, t.shift);
-  const int limit = t.top_k ? min(t.top_k, t.n) : t.n;
-  uint64_t x[2], m[2], Z;
-  bool stays[2];
+  const int limit = t.top_k ? min(t.top_k, t.n) : t.n, warps = warps_of(t.n);
+  uint64_t x[2] = {0, 0}, m[2] = {0, 0}, Z;
+  bool stays[2] = {false, false};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    x[q] = at + q < t.n ? s.mine[at + q] : 0;
-    const double w = at + q < t.n ? t.weight(logit_of(x[q])) : 0.;
+    if (at + q >= t.n) break;
+    x[q] = s.mine[at + q];
+    const double w = t.weight(logit_of(x[q]));
     stays[q] = at + q < limit && (at + q == 0 || w >= t.min_w);
     m[q] = Weight::to_fixed(w);
     if (at + q == t.n - 1) s.found = w < t.min_w || p.V <= kAll;
   }
-  const uint64_t before = sum_before(s, m[0] + m[1], Z);
+  const uint64_t before = sum_before(s, m[0] + m[1], warps, Z);
   if (at == limit - 1) s.found_mass = before + m[0];
   if (at + 1 == limit - 1) s.found_mass = before + m[0] + m[1];
   __syncthreads();
@@ -318,7 +326,7 @@ __device__ __forceinline__ bool draw_from_list(Shared &s, const SampleParams &p,
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 2; ++q) m[q] = at + q < t.n ? s.key[at + q] : 0;
-  const uint64_t below = sum_before(s, m[0] + m[1], Z), to = target_of(t.u, Z);
+  const uint64_t below = sum_before(s, m[0] + m[1], warps, Z), to = target_of(t.u, Z);
   if (below <= to && to < below + m[0] + m[1]) {
     const uint64_t y = s.mine[at + (to < below + m[0] ? 0 : 1)];
     p.token[row] = index_of(y);

@@ -351,3 +351,21 @@ def test_lists_of_hundreds(nslm, B, V, dtype):
         for t in (0.05, 1.0, 5.0):
             _check(nslm, l, u, t=_full(B, t), top_k=ks)
         _check(nslm, l, u, top_k=ks, top_p=_full(B, 0.95), min_p=_full(B, 0.001))
+
+
+def test_thousands_of_infinite_logits_and_settings_left_out(nslm):
+    B, V = 4, 20000
+    l = _logits(B, V, 31)
+    l[0, ::4] = float("inf")                        # more than a list holds
+    l[1, :900] = float("inf")
+    l[2, 3:] = -float("inf")
+    u = torch.rand(B, generator=_gen(6), device="cuda")
+    _check(nslm, l, u)
+    for k in (2, 500, 2000, 7000):
+        _check(nslm, l, u, top_k=_full(B, k, torch.int32))
+        _check(nslm, l, u, top_k=_full(B, k, torch.int32), top_p=_full(B, 0.5))
+    _check(nslm, l, u, top_p=_full(B, 0.25), min_p=_full(B, 0.5))
+    # a struct of no arrays is no struct
+    token = guard.buffer(B, torch.int32, fill=-7)
+    nslm.nslm_sample(l, nslm.NSLM_TYPE_F32, B, V, V, nslm.sample_params(), u, token)
+    assert np.array_equal(token.cpu().numpy(), _want(l, u)[0])
