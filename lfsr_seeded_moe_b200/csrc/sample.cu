@@ -45,14 +45,14 @@ struct SampleParams {
 // fp32 (RES).  Of a larger batch it takes a longer part, which passes through
 // small rings of its warps each time it is needed, from the L2 after the first:
 // then a row's barriers, about 1 us each, are shared by more logits, and the
-// whole batch runs at once (64 x 131072 with top-k 50: 34 us kept, 24 streamed).
+// whole batch runs at once (64 x 131072 with top-k 50: 34 us kept, 23 streamed).
 //
 // w is 64-bit fixed point with 44 bits behind the point, at most 2^18 of them,
 // so sums stay below 2^62 and are exact: whatever order threads and CTAs add in,
 // the same u gives the same token.
 //
-// One row of 32003 logits with top-k 50 and top-p takes 8.7 us, nearly all of it
-// the cluster's barriers; 64 x 131072 without a filter 31 us, bound by the
+// One row of 32003 logits with top-k 50 and top-p takes 8.1 us, nearly all of it
+// latency: its load, four exchanges, the list's sort and sums; 64 x 131072 without a filter 31 us, bound by the
 // instructions of two passes (0.62 of the issue slots, DRAM at 15%).
 
 // Weights in units of 2^-44.  exp(x) = 2^(k/16) e^r, |r| <= ln 2 / 32, with the
