@@ -39,7 +39,7 @@
  *    caller owns every buffer, the workspace included; the library never
  *    allocates, frees or synchronises.  All work is enqueued on `stream`
  *    (a cudaStream_t; NULL means the legacy default stream) and completes
- *    asynchronously.
+ *    asynchronously.  Stream and buffers belong to the caller's current device.
  *  - Arguments are checked on the host before anything is launched; a bad
  *    argument returns a negative status and launches nothing.  A launch
  *    failure returns NSLM_ERR_CUDA (the CUDA error is consumed).

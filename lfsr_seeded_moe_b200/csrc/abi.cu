@@ -24,7 +24,8 @@ struct SmemEntry {
   int device;
   size_t bytes;
 };
-SmemEntry g_smem[256];
+constexpr int kSmemEntries = 1024;  // kernels (nslm_q4_gemv alone has 120 forms) times devices
+SmemEntry g_smem[kSmemEntries];
 int g_smem_n = 0;
 std::mutex g_mu;
 
@@ -70,7 +71,7 @@ int32_t ensure_smem(const void *kernel, size_t bytes) {
       g_smem[i].bytes = bytes;
       return NSLM_OK;
     }
-  if (g_smem_n < 256) g_smem[g_smem_n++] = SmemEntry{kernel, dev, bytes};
+  if (g_smem_n < kSmemEntries) g_smem[g_smem_n++] = SmemEntry{kernel, dev, bytes};
   return NSLM_OK;
 }
 
