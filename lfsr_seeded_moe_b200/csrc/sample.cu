@@ -416,6 +416,7 @@ template <class T, bool RES> struct Row {
       // the warp's share by 16-byte copies from the last aligned address before
       // it; bytes past its end are zeros
       constexpr int kOf = kRingChunk / sizeof(T);
+      static_assert(kRingChunk % 512 == 0 && kOf % (32 * U) == 0, "lanes go through a chunk in whole steps");
       const int lo = min(n, warp * share()), hi = min(n, lo + share());
       const int before = (int)(((uintptr_t)(src + lo) & 15) / sizeof(T));
       const char *from = reinterpret_cast<const char *>(src + lo - before);
