@@ -35,8 +35,8 @@ __device__ __forceinline__ float bf16_f32(uint32_t h) { return __uint_as_float(h
 // over the groups, [b s] times [x's sum, 8 times that], with b and s as they are
 // stored (bf16) and the sums in three bf16 parts (24 bits): 3 mma a stage.
 //
-// 131072 x 4096 with groups of 64 takes 65 us with one vector and 67 to 75 with
-// 8 (306 MB: 47 at the copy rate), 50257 x 2048 15.5 (8.8).  Copies alone take
+// 131072 x 4096 with groups of 64 takes 65 us with one vector and 68 with 8 (306
+// MB: 47 at the copy rate; 75 to 80 in runs of thousands), 50257 x 2048 15.5 (8.8).  Copies alone take
 // 48 to 55 us of the first, computing alone 52 to 62 (the unpacking's shifts and
 // masks on the ALU pipe), and they overlap but for the rest.  512 x 1024 takes
 // 2 us, a launch and a load.
