@@ -43,6 +43,12 @@ int32_t check_matrix(const nslm_seed_matrix *W);
 // of nslm_moe_seed_ffn_static on the current device.
 int32_t static_scratch_status_word(const int32_t **out);
 
+// A CTA may touch another's shared memory only once all CTAs of the cluster run.
+// Every thread arrives at its kernel's start, and waits before the first remote
+// access: what lies between hides the barrier.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // Workspace of nslm_moe_balance.
 size_t balance_ws_bytes(int32_t T, int32_t E);
 

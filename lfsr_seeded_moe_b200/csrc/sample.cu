@@ -770,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   Shared &s = *reinterpret_cast<Shared *>(smem);
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  if (ctas > 1) cluster_arrive();
   const int row = blockIdx.x / ctas, tid = threadIdx.x;
   const int first = min(p.V, rank * p.len), n = min(p.V - first, p.len);
   if (tid < 16) s.pow16[tid] = exp2((double)tid / 16.) * 0x1p44;
@@ -826,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // The largest logits of kGroups parts of the row, in every CTA: `width` threads have one.
   const int width = kThreads / kGroups * ctas;
   for (int o = 1; o < width; o <<= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  if (ctas > 1) cluster_wait();  // all run: group_max is the first that goes to the others
   if (tid % width < ctas) {
     float *to = ctas == 1 ? s.group_max : cluster.map_shared_rank(s.group_max, tid % width);
     to[rank * (kGroups / ctas) + tid / width] = hi;
