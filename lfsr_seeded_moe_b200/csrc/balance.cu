@@ -201,6 +201,7 @@ struct Finish {
 
 // The end, by a cluster whose CTAs have a slice of the experts each: part(g, e)
 // and tokens(g, e) give the sums and counts of g's tokens, e = E their number.
+// All CTAs of the cluster have to run by then: it stores into their shared memory.
 template <class P, class C> __device__ void finish(const BalanceParams &p, Finish &s, int parts, P part, C tokens) {
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
@@ -316,8 +317,10 @@ template <class Tok> __global__ void __launch_bounds__(kPartThreads) balance_par
 __global__ void __launch_bounds__(kThreads) balance_finish_kernel(const BalanceParams p) {
   extern __shared__ double smem[];
   Finish &s = *reinterpret_cast<Finish *>(smem);
+  cluster_arrive();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cluster_wait();  // finish() stores into the others
   finish(
       p, s, p.parts, [&](int g, int e) { return p.part_p[(size_t)g * p.E + e]; },
       [&](int g, int e) { return p.part_c[(size_t)g * (p.E + 1) + e]; });

@@ -25,6 +25,7 @@ def _body(source, kernel):
 
 @pytest.mark.parametrize("source,kernel,remote", [
     ("sample.cu", "sample_kernel", "map_shared_rank"),
+    ("balance.cu", "balance_finish_kernel", "finish("),
 ])
 def test_the_cluster_runs_before_the_first_remote_access(source, kernel, remote):
     body = _body(source, kernel)
