@@ -2,6 +2,7 @@
 // top-k, top-p and min-p, at given random numbers.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -91,12 +92,14 @@ struct Weight {
   }
 };
 
-// A token of a list: its logit in the order of its values, then its index
-// falling, so that of two the larger comes first.
-__device__ __forceinline__ uint64_t key_of(float v, int i) {
+// A logit's place among all fp32 values.
+__device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);  // -0 as 0
-  return (uint64_t)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | ~(uint32_t)i;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+// A token of a list: its logit's place, then its index falling, so that of two
+// the larger comes first.
+__device__ __forceinline__ uint64_t key_of(float v, int i) { return (uint64_t)order_of(v) << 32 | ~(uint32_t)i; }
 __device__ __forceinline__ int index_of(uint64_t key) { return (int)~(uint32_t)key; }
 __device__ __forceinline__ float logit_of(uint64_t key) {
   const uint32_t k = (uint32_t)(key >> 32);
@@ -342,22 +345,31 @@ struct Range {
   int bin = -1;        // of those, the ones in this bin of [lo, hi], or all
   uint64_t above = 0;  // the count or mass of the kept tokens that come before
 
-  // Falls from 0 at hi to kBins - 1 at lo, for any lo < hi: where hi - lo is so
-  // small that `scale` is infinite, hi is in bin 0 and all others in the last.
+  // A bin falls from 0 at hi to kBins - 1 at lo, for any lo < hi.  Bins are
+  // equally wide in three rounds, which part all but values of many magnitudes,
+  // unless hi - lo is so small that `scale` is infinite.  Then they have 2^shift
+  // neighbouring fp32 values each: of 2^32 at most a bin has 2^20, 2^8 and one,
+  // so another three rounds end at a single value, whatever the logits.
+  static constexpr int kEvenRounds = 3;
   float half = 1.f, scale = 0.f;
-  __device__ __forceinline__ void set_bins() {
+  int shift = -1;  // -1: equally wide
+  __device__ __forceinline__ void set_bins(int round) {
+    static_assert(kBins == 1 << 12);
     half = hi - lo < INFINITY ? 1.f : 0.5f;
     scale = kBins / (hi * half - lo * half);
+    shift = round < kEvenRounds && scale < INFINITY ? -1 : max(0, 32 - __clz(order_of(hi) - order_of(lo)) - 12);
     bin = -1;
   }
-  __device__ __forceinline__ int bin_of(float v) const {
+  template <bool EVEN> __device__ __forceinline__ int bin_as(float v) const {
+    if (!EVEN) return (int)((order_of(hi) - order_of(v)) >> shift);
     return min(kBins - 1, (int)(__fmaf_rn(-half, v, hi * half) * scale));
   }
+  __device__ __forceinline__ int bin_of(float v) const { return shift < 0 ? bin_as<true>(v) : bin_as<false>(v); }
   // The chosen bin's tokens lie between lo and top too; these are bounds that
   // are a little wide, to see most others without their bin.
   __device__ __forceinline__ void set_bin(int b) {
     bin = b;
-    if (!(scale < 1e30f)) return;  // the bounds themselves would be rounded away
+    if (shift >= 0 || !(scale < 1e30f)) return;  // the bounds themselves would be rounded away
     const float eps = 0x1p-20f * (fabsf(hi) + fabsf(lo)) * half, of = hi * half, width = 1.f / scale;
     lo = fmaxf(lo, (of - ((b + 1.01f) * width + eps)) / half);
     if (b > 0) top = fminf(top, (of - ((b - 0.01f) * width - eps)) / half);
@@ -609,15 +621,15 @@ template <class T, bool RES> struct Row {
   // to reach need all stay.
   __device__ __forceinline__ void cut(uint64_t need, bool by_mass, Range r) {
     auto inside = [&](int i, float v) { return r.has(v) && kept(i, v); };
-    while (r.lo < r.hi) {
+    for (int round = 0; r.lo < r.hi; ++round) {
       // a histogram of the range; the bin that has the token is the next range
-      r.set_bins();
+      r.set_bins(round);
       __syncthreads();
       for (int b = threadIdx.x; b < kBins; b += kThreads) s.hist.lo[b] = s.hist.hi[b] = 0;
       __syncthreads();
-      each<2>([&](int i, float v) {
+      auto count = [&](auto even, int i, float v) {
         if (!inside(i, v)) return;
-        const int b = r.bin_of(v);
+        const int b = r.template bin_as<decltype(even)::value>(v);
         if (by_mass) {
           const uint64_t x = w.fixed(v);
           const uint32_t lo = (uint32_t)x, old = atomicAdd(&s.hist.lo[b], lo);
@@ -626,7 +638,9 @@ template <class T, bool RES> struct Row {
         } else {
           atomicAdd(&s.hist.lo[b], 1u);
         }
-      });
+      };
+      if (r.shift < 0) each<2>([&](int i, float v) { count(std::true_type{}, i, v); });
+      else each<2>([&](int i, float v) { count(std::false_type{}, i, v); });
       sync_row();
       // each CTA adds its part of all histograms
       // (kBins / ctas bins of all; always kPer values a thread, so that their
