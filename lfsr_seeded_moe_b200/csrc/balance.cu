@@ -102,8 +102,16 @@ template <int LANES, int NV, bool VEC> struct Token {
 //
 // The CTA's tokens of a grid of `ctas`: the probabilities' sums to s_p[E], the
 // counts and the number of tokens to s_c[E + 1].  s_w: a row of E for each warp.
-template <class Tok, int THREADS>
-__device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, int ctas, float *s_w, float *s_p, int32_t *s_c) {
+//
+// A lane adds kBlock probabilities in fp32, the warps join theirs (2 + 24 more
+// additions), and blocks add up in fp64: equal probabilities are rounded the
+// same way again and again, which in one fp32 sum of the thousands of tokens
+// that a lane may have would be 1e-4 and more of it.  65536 tokens are one block.
+// SUM: float where one block is all there is, else double.
+constexpr int kBlock = 64;
+
+template <class Tok, int THREADS, class SUM>
+__device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, int ctas, float *s_w, SUM *s_p, int32_t *s_c) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kWarps = THREADS / 32, kRows = Tok::kTokens * kWarps;
   float z[Tok::kNV];
@@ -146,42 +154,48 @@ __device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, in
   }
   n = __reduce_add_sync(0xffffffffu, n);
   if (lane == 0 && n) atomicAdd(&s_c[p.E], n);
-  float acc[Tok::kNV] = {};
-  for (int t0 = cta * kRows; t0 < p.T;) {
-    Tok::exps(z);
-    float d = 0.f;
+  constexpr bool kOne = std::is_same<SUM, float>::value;
+  static_assert(!kOne || kOneLaunchT <= kBlock * kWarps);
+  for (int t0 = cta * kRows, block = 0;; ++block) {
+    float acc[Tok::kNV] = {};
+    for (int i = 0; (kOne || i < kBlock) && t0 < p.T; ++i) {
+      Tok::exps(z);
+      float d = 0.f;
 #pragma unroll
-    for (int j = 0; j < Tok::kNV; ++j) d += z[j];
-    d = Tok::sum(d);
-    const float r = d == 0.f ? 0.f : 1.f / d;  // nothing left in the row: nothing to add
+      for (int j = 0; j < Tok::kNV; ++j) d += z[j];
+      d = Tok::sum(d);
+      const float r = d == 0.f ? 0.f : 1.f / d;  // nothing left in the row: nothing to add
 #pragma unroll
-    for (int j = 0; j < Tok::kNV; ++j) acc[j] = fmaf(z[j], r, acc[j]);
-    t0 += ctas * kRows;
-    if (t0 < p.T) fetch(t0 + mine);
-  }
-  // over the warp's tokens: each halving leaves a lane half of the columns
-  int keep = Tok::kNV, from = 0;
-#pragma unroll
-  for (int o = 16; o >= 32 / Tok::kTokens; o >>= 1) {
-    keep /= 2;
-    const bool up = lane & o;
-#pragma unroll
-    for (int j = 0; j < Tok::kNV / 2; ++j) {
-      if (j >= keep) break;
-      const float other = __shfl_xor_sync(0xffffffffu, up ? acc[j] : acc[j + keep], o);
-      acc[j] = (up ? acc[j + keep] : acc[j]) + other;
+      for (int j = 0; j < Tok::kNV; ++j) acc[j] = fmaf(z[j], r, acc[j]);
+      t0 += ctas * kRows;
+      if (t0 < p.T) fetch(t0 + mine);
     }
-    from += up ? keep : 0;
-  }
+    // over the warp's tokens: each halving leaves a lane half of the columns
+    int keep = Tok::kNV, from = 0;
 #pragma unroll
-  for (int j = 0; j < Tok::kNV / Tok::kTokens; ++j)
-    if (Tok::column(from + j) < p.E) s_w[warp * p.E + Tok::column(from + j)] = acc[j];
-  __syncthreads();
-  for (int e = tid; e < p.E; e += THREADS) {
-    float q = 0;
+    for (int o = 16; o >= 32 / Tok::kTokens; o >>= 1) {
+      keep /= 2;
+      const bool up = lane & o;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) q += s_w[w * p.E + e];
-    s_p[e] = q;
+      for (int j = 0; j < Tok::kNV / 2; ++j) {
+        if (j >= keep) break;
+        const float other = __shfl_xor_sync(0xffffffffu, up ? acc[j] : acc[j + keep], o);
+        acc[j] = (up ? acc[j + keep] : acc[j]) + other;
+      }
+      from += up ? keep : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < Tok::kNV / Tok::kTokens; ++j)
+      if (Tok::column(from + j) < p.E) s_w[warp * p.E + Tok::column(from + j)] = acc[j];
+    __syncthreads();
+    for (int e = tid; e < p.E; e += THREADS) {
+      float q = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) q += s_w[w * p.E + e];
+      s_p[e] = kOne || block == 0 ? q : s_p[e] + q;
+    }
+    if (kOne || t0 >= p.T) break;
+    __syncthreads();  // s_w is written again
   }
 }
 
@@ -280,8 +294,12 @@ template <class P, class C> __device__ void finish(const BalanceParams &p, Finis
   }
 }
 
-// Shared memory: a row of E sums for each warp, then [E] and [E + 1] of the CTA.
-size_t balance_smem(int E, int threads) { return ((size_t)threads / 32 * E + E + E + 1) * 4; }
+// Shared memory: a row of E sums for each warp, then [E] (of SUM, which an even
+// number of warps aligns) and [E + 1] of the CTA.
+template <class SUM> size_t balance_smem(int E, int threads) {
+  return (size_t)threads / 32 * E * 4 + E * sizeof(SUM) + ((size_t)E + 1) * 4;
+}
+static_assert(kThreads / 32 % 2 == 0 && kPartThreads / 32 % 2 == 0);
 
 // Few tokens: one cluster does it all.
 template <class Tok> __global__ void __launch_bounds__(kThreads) balance_one_kernel(const BalanceParams p) {
@@ -294,7 +312,7 @@ template <class Tok> __global__ void __launch_bounds__(kThreads) balance_one_ker
   float *s_p = s_w + kThreads / 32 * p.E;
   int32_t *s_c = reinterpret_cast<int32_t *>(s_p + p.E);
   const int ctas = (int)cluster.num_blocks();
-  count_tokens<Tok, kThreads>(p, (int)cluster.block_rank(), ctas, s_w, s_p, s_c);
+  count_tokens<Tok, kThreads, float>(p, (int)cluster.block_rank(), ctas, s_w, s_p, s_c);
   sync_cluster(ctas);
   finish(
       p, s, ctas, [&](int g, int e) { return cluster.map_shared_rank(s_p, g)[e]; },
@@ -306,11 +324,11 @@ template <class Tok> __global__ void __launch_bounds__(kPartThreads) balance_par
   float *s_w = reinterpret_cast<float *>(smem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  float *s_p = s_w + kPartThreads / 32 * p.E;
+  double *s_p = reinterpret_cast<double *>(s_w + kPartThreads / 32 * p.E);
   int32_t *s_c = reinterpret_cast<int32_t *>(s_p + p.E);
-  count_tokens<Tok, kPartThreads>(p, blockIdx.x, gridDim.x, s_w, s_p, s_c);
+  count_tokens<Tok, kPartThreads, double>(p, blockIdx.x, gridDim.x, s_w, s_p, s_c);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kPartThreads) p.part_p[(size_t)blockIdx.x * p.E + e] = s_p[e];
+  for (int e = threadIdx.x; e < p.E; e += kPartThreads) p.part_p[(size_t)blockIdx.x * p.E + e] = (float)s_p[e];
   for (int e = threadIdx.x; e <= p.E; e += kPartThreads) p.part_c[(size_t)blockIdx.x * (p.E + 1) + e] = s_c[e];
 }
 
@@ -456,7 +474,7 @@ extern "C" int32_t nslm_moe_balance(const float *logits, const int32_t *ids, con
     int ctas = 1;
     while (ctas < kCluster && (T > 64 * ctas || ceil_div(E, ctas) + 1 > kThreads)) ctas *= 2;
     st = with_token(E, [&](auto tok) {
-      return launch(balance_one_kernel<decltype(tok)>, ctas, ctas, kThreads, sizeof(Finish) + balance_smem(E, kThreads), s, p);
+      return launch(balance_one_kernel<decltype(tok)>, ctas, ctas, kThreads, sizeof(Finish) + balance_smem<float>(E, kThreads), s, p);
     });
     if (st == NSLM_OK) g_launches = 1;
     return st;
@@ -466,7 +484,7 @@ extern "C" int32_t nslm_moe_balance(const float *logits, const int32_t *ids, con
   st = with_token(E, [&](auto tok) {
     using Tok = decltype(tok);
     p.parts = std::min({ceil_div(T, Tok::kTokens * kPartThreads / 32), num_sms(), kMaxCtas});
-    return launch(balance_part_kernel<Tok>, p.parts, 1, kPartThreads, balance_smem(E, kPartThreads), s, p);
+    return launch(balance_part_kernel<Tok>, p.parts, 1, kPartThreads, balance_smem<double>(E, kPartThreads), s, p);
   });
   if (st == NSLM_OK) st = launch(balance_finish_kernel, kCluster, kCluster, kThreads, sizeof(Finish), s, p);
   if (st == NSLM_OK) g_launches = 2;
