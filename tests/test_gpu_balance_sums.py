@@ -91,3 +91,24 @@ def test_blocks_of_tokens(nslm, T, E, k):
     want, M = _mean(z)
     assert np.array_equal(counts[:E], torch.bincount(ids.reshape(-1).long(), minlength=E).cpu().numpy())
     _check(counts, mean, loss, want, M, T, E, k)
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 100, 8), (513, 1024, 8), (1024, 100, 8), (1025, 64, 2), (14208, 128, 4),
+                                   (28417, 100, 4), (65536, 128, 8), (65537, 128, 8), (14209, 200, 4), (10657, 600, 8),
+                                   (909313, 64, 1)])
+def test_no_token_is_lost_or_counted_twice(nslm, T, E, k):
+    # tokens at the ends of rounds and blocks have an expert each to themselves,
+    # which then makes most of that expert's mean
+    g = torch.Generator("cuda").manual_seed(T)
+    F = _in_flight(E)
+    at = sorted({t for i in (0, 1, 2, 63, 64) for t in (i * F - 1, i * F) if 0 <= t < T} | {0, T // 2, T - 1})
+    z = torch.randn(T, E, generator=g, device="cuda")
+    z[:, :len(at)] -= 8
+    for e, t in enumerate(at):
+        z[t, e] = 12
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    counts, mean, loss = _run(nslm, z, ids, E, k)
+    want, M = _mean(z)
+    rel = _bound(M, T, E)
+    assert np.all(want[:len(at)] * T * rel < 0.1)  # a token more or less would be seen
+    _check(counts, mean, loss, want, M, T, E, k)
