@@ -228,7 +228,8 @@ int32_t nslm_moe_balance(const float *logits, const int32_t *ids, const uint8_t 
  *   f_e = c_e / (k n)
  * and zeros in the rows of tokens that do not count.  counts: int32 [E + 1] as
  * nslm_moe_balance wrote them (a data-parallel caller may sum c_e and n over
- * its ranks first: the gradient is then that of the whole batch's loss);
+ * its ranks first, while each stays below 2^31: the gradient is then that of
+ * the whole batch's loss);
  * dloss: fp32 [1], device, the gradient that arrives at the loss, or NULL for
  * 1; dlogits: fp32 [T][E], written whole; it may be logits itself.
  * One launch, no workspace. */

@@ -355,7 +355,7 @@ template <class Tok>
 __global__ void __launch_bounds__(kGradThreads)
     balance_grad_kernel(const float *logits, const int32_t *counts, const uint8_t *mask, int T, int E, int k, float coef,
                         const float *dloss, float *dlogits) {
-  __shared__ int32_t s_total[kGradThreads / 32];
+  __shared__ uint32_t s_total[2][kGradThreads / 32];
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -369,17 +369,18 @@ __global__ void __launch_bounds__(kGradThreads)
   };
   int t = blockIdx.x * kRows + tid / (32 / Tok::kTokens);
   fetch(t);
-  int total = 0;
-  for (int e = tid; e < E; e += kGradThreads) total += counts[e];
-  total = __reduce_add_sync(0xffffffffu, total);
-  if ((tid & 31) == 0) s_total[tid >> 5] = total;
+  // counts summed over ranks fit 32 bits, their total need not: halves of 16 bits, a total of each
+  uint32_t low = 0, high = 0;
+  for (int e = tid; e < E; e += kGradThreads) low += counts[e] & 0xffff, high += counts[e] >> 16;
+  low = __reduce_add_sync(0xffffffffu, low), high = __reduce_add_sync(0xffffffffu, high);
+  if ((tid & 31) == 0) s_total[0][tid >> 5] = low, s_total[1][tid >> 5] = high;
   const double n = max(1, counts[E]);
   const float scale = (float)((dloss ? (double)dloss[0] : 1.0) * coef * E / n);
   __syncthreads();
-  total = 0;
+  low = high = 0;
 #pragma unroll
-  for (int w = 0; w < kGradThreads / 32; ++w) total += s_total[w];
-  const double mean = (double)total / E, share = 1. / (k * n);
+  for (int w = 0; w < kGradThreads / 32; ++w) low += s_total[0][w], high += s_total[1][w];
+  const double mean = (high * 65536. + low) / E, share = 1. / (k * n);
   float f[Tok::kNV];
 #pragma unroll
   for (int j = 0; j < Tok::kNV; ++j) f[j] = Tok::column(j) < E ? (float)((counts[Tok::column(j)] - mean) * share) : 0.f;

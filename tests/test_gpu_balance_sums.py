@@ -112,3 +112,29 @@ def test_no_token_is_lost_or_counted_twice(nslm, T, E, k):
     rel = _bound(M, T, E)
     assert np.all(want[:len(at)] * T * rel < 0.1)  # a token more or less would be seen
     _check(counts, mean, loss, want, M, T, E, k)
+
+
+@pytest.mark.parametrize("E,k", [(8, 8), (100, 8), (1023, 2)])
+def test_gradient_with_counts_of_many_ranks(nslm, E, k):
+    # counts summed over ranks: each below 2^31, their total far above, and nearly
+    # even, so that nothing is left of their differences unless their mean is taken
+    # off first.  f_e less the mean is rounded once; with it a value has the errors
+    # of two probabilities (each (2 (3M + 4) + 38) h) and of the dot product's sum
+    # (37 h), its centring (h) and five products.
+    T = 9
+    g = torch.Generator("cuda").manual_seed(E)
+    z = torch.randn(T, E, generator=g, device="cuda")
+    c = 2**30 + torch.randint(-2000, 2000, (E,), generator=g, device="cuda")
+    assert int(c.sum()) > 2**31
+    n = min(int(c.sum()) // k, 2**31 - 1)
+    counts = torch.cat([c, c.new_tensor([n])]).to(torch.int32)
+    d = guard.buffer((T, E), torch.float32, fill=float("nan"))
+    nslm.nslm_moe_balance_grad(z, counts, None, T, E, k, 0.5, None, d)
+    y = z.double() - z.double().amax(1, keepdim=True)
+    p = torch.exp(y) / torch.exp(y).sum(1, keepdim=True)
+    f = (c.double() - c.double().mean()) / (k * n)
+    scale = 0.5 * E / n
+    want = scale * p * (f - (p * f).sum(1, keepdim=True))
+    size = scale * p * (f.abs() + (p * f.abs()).sum(1, keepdim=True))
+    rel = (2 * (2 * (3 * float(-y.min()) + 4) + 38) + 37 + 1 + 5) * 2.0 ** -24
+    assert bool(((d.double() - want).abs() <= rel * size + 1e-44).all()), float(((d.double() - want).abs() / size).max())
