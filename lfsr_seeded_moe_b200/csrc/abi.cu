@@ -24,7 +24,7 @@ struct SmemEntry {
   int device;
   size_t bytes;
 };
-constexpr int kSmemEntries = 1024;  // kernels (nslm_q4_gemv alone has 120 forms) times devices
+constexpr int kSmemEntries = 1024;  // kernels (nslm_q4_gemv alone has 100 forms) times devices
 SmemEntry g_smem[kSmemEntries];
 int g_smem_n = 0;
 std::mutex g_mu;

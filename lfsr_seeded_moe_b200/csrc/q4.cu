@@ -365,6 +365,12 @@ int32_t check_q4(const nslm_q4_matrix *W) {
 
 constexpr size_t kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of an SM, and of that for each CTA
 
+template <int G, bool AFFINE> constexpr size_t q4_smem(int mp, int K, int warps, int stages) {
+  const int NS = (K + kStageK - 1) / kStageK;
+  return kZero + (size_t)2 * mp * K + (AFFINE ? ((size_t)6 * mp * (NS * kSums<G> + 8) + 127) / 128 * 128 : 0) +
+         (size_t)warps * stages * kSlot<AFFINE> + (size_t)2 * warps * kMaxVec * kTile * 4;
+}
+
 // Splits the work for CTAs of `warps` and gives their shared memory.
 template <int G, bool AFFINE> size_t q4_plan(Q4Params &p, int mp, int warps, int stages) {
   // the split of K with the least rounds of work: stages of a warp, and what a
@@ -381,8 +387,7 @@ template <int G, bool AFFINE> size_t q4_plan(Q4Params &p, int mp, int warps, int
     if (cost < best) best = cost, p.kw = kw;
   }
   p.steps = ceil_div(tiles, warps / p.kw);
-  return kZero + (size_t)2 * mp * p.W.K + (AFFINE ? ((size_t)6 * mp * (p.NS * kSums<G> + 8) + 127) / 128 * 128 : 0) +
-         (size_t)warps * stages * kSlot<AFFINE> + (size_t)2 * warps * kMaxVec * kTile * 4;
+  return q4_smem<G, AFFINE>(mp, p.W.K, warps, stages);
 }
 
 template <int G, int MP, int WARPS, int STAGES, bool AFFINE>
@@ -404,7 +409,8 @@ int32_t launch_q4_as(const Q4Params &p, size_t smem, cudaStream_t s) {
 }
 
 // Two CTAs of 8 warps on an SM where the activations leave room for both, else
-// one of 16, or of 14 or 12 with a shorter ring for the longest rows.
+// one of 16, or of 14 with a shorter ring for the longest rows; of 12 where not
+// even those fit, which is groups of 32 with offsets (their sums take 24 KB).
 template <int G, int MP, bool AFFINE>
 int32_t launch_q4(Q4Params p, cudaStream_t s) {
   size_t smem = q4_plan<G, AFFINE>(p, MP, 8, 4);
@@ -414,9 +420,15 @@ int32_t launch_q4(Q4Params p, cudaStream_t s) {
   smem = q4_plan<G, AFFINE>(p, MP, 16, 3);
   if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 16, 3, AFFINE>(p, smem, s);
   smem = q4_plan<G, AFFINE>(p, MP, 14, 2);
-  if (smem + kSmemReserved <= kSmemPerSm) return launch_q4_as<G, MP, 14, 2, AFFINE>(p, smem, s);
-  smem = q4_plan<G, AFFINE>(p, MP, 12, 2);
-  return launch_q4_as<G, MP, 12, 2, AFFINE>(p, smem, s);
+  constexpr bool kFits = q4_smem<G, AFFINE>(MP, kMaxMK / MP, 14, 2) + kSmemReserved <= kSmemPerSm;
+  if constexpr (!kFits) {
+    static_assert(q4_smem<G, AFFINE>(MP, kMaxMK / MP, 12, 2) + kSmemReserved <= kSmemPerSm);
+    if (smem + kSmemReserved > kSmemPerSm) {
+      smem = q4_plan<G, AFFINE>(p, MP, 12, 2);
+      return launch_q4_as<G, MP, 12, 2, AFFINE>(p, smem, s);
+    }
+  }
+  return launch_q4_as<G, MP, 14, 2, AFFINE>(p, smem, s);
 }
 
 template <int G, int MP>
