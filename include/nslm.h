@@ -167,7 +167,9 @@ int32_t nslm_seed_gemv_flags(const nslm_seed_matrix *W, const uint16_t *x_bf16, 
  *   y[m][i] = sum_k W[i][k] * x[m][k],  m < M, i < N.
  * x: bf16 [M][K]; y: fp32 [M][N]; 1 <= M <= 8; M, rounded up to 1, 2, 4 or 8,
  * times K is at most 65536 (the activations stay in shared memory).  Products
- * are exact, sums are held in fp32; the weights are never rounded.  Finite x.
+ * are exact, sums are held in fp32; the weights are never rounded.  x: finite,
+ * magnitudes up to 2^117, since a group's sums of (q - 8) x and of 8 x are taken
+ * before its scale; 8 s x and b x, summed over a row, stay within fp32 too.
  * flags: 0 or NSLM_GEMV_FIELDS_READY, with the meaning of nslm_seed_gemv_flags
  * (no kernel enqueued earlier on `stream` writes W's q, scales or biases);
  * other bits return NSLM_ERR_ARG.  The result does not depend on timing (no

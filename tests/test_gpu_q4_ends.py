@@ -49,3 +49,20 @@ def test_the_longest_rows(nslm, M, G, affine):
             nslm.nslm_q4_gemv(nslm.q4_matrix(q, scales, biases, G), x, M, y)
             # at most 2^16 terms of up to 46 (15 times 2, and 16 that an offset is taken apart by): below 2^22
             assert torch.equal(y.double(), x.double() @ _dense(q, scales, biases, G).t()), (K, N)
+
+
+@pytest.mark.parametrize("affine", [True, False])
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_the_largest_activations(nslm, G, affine):
+    # a group's sums before the scale reach 128 * 8 * 2^117 = 2^127; small scales bring the rows back
+    N, K = 40, 1024
+    q, scales, biases = _weights(N, K, G, affine, G, exponent=-40)
+    g = torch.Generator("cuda").manual_seed(G)
+    x = torch.randint(-1, 2, (3, K), generator=g, device="cuda")
+    x[0], x[1] = 1, -1
+    q[0] = 0                                         # every weight the lowest
+    x = (x * 2.0 ** 100 * 2.0 ** 17).bfloat16()
+    y = guard.buffer((3, N), torch.float32, fill=float("nan"))
+    nslm.nslm_q4_gemv(nslm.q4_matrix(q, scales, biases, G), x, 3, y)
+    assert bool(torch.isfinite(y).all())
+    assert torch.equal(y.double(), x.double() @ _dense(q, scales, biases, G).t())
