@@ -151,16 +151,24 @@ def _p(x) -> int:
     return x.data_ptr()
 
 
-_torch = None  # imported by the first call that needs the current stream
+_current_stream = None  # made by the first call that needs the current stream
+
+
+def _stream_getter():
+    import torch
+    # the handle alone: current_stream() builds a Stream object, 3 us of a call's 8
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    if raw is None:  # not part of torch's public interface
+        return lambda: int(torch.cuda.current_stream().cuda_stream)
+    return lambda: raw(device())
 
 
 def _s(stream) -> int:
     if stream is None:
-        global _torch
-        if _torch is None:
-            import torch as _torch
-        # the handle alone: current_stream() builds a Stream object, 3 us of a call's 8
-        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _stream_getter()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
