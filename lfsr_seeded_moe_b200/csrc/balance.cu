@@ -15,7 +15,10 @@ namespace cg = cooperative_groups;
 constexpr int kMaxE = 1024;
 constexpr int kThreads = 512;
 constexpr int kCluster = 8;
-constexpr int kOneLaunchT = 1024;  // up to here one cluster does it all, and there is no workspace
+// Up to here one cluster does it all, and a caller needs no workspace.  One
+// launch and two, measured at 1024 tokens: 100 experts 5.6 and 6.3 us, 256 7.4
+// and 6.6, 512 11.2 and 7.8, 1024 15.3 and 10.8.
+constexpr int kOneLaunchT = 1024;
 constexpr int kPartThreads = 768;  // leaves the CTAs of the end their registers, so that they wait on their SMs
 constexpr int kMaxCtas = 148;      // CTAs that leave parts in the workspace
 

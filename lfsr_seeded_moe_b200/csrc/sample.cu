@@ -26,7 +26,8 @@ constexpr int kGroups = 128;              // parts of a row whose largest logits
 constexpr int kListAt = 96;               // the last of those, in descending order, from which a top-k's list begins
 // The one from which on a list is made for top-p: 266 tokens on average.  At 96
 // (177) it costs 1 to 3% less, at 120 (355) as much more; a row whose top-p is
-// past its list costs 20 us and more.
+// past its list costs 20 us and more.  Of rows of 32000 with some tens of likely
+// tokens 45, 39 and 35% are past the three with top-p 0.9; of 131072 92, 92 and 91%.
 constexpr int kListMass = 112;
 
 struct SampleParams {
