@@ -261,9 +261,13 @@ int32_t bounds_error_moe();
 int32_t bounds_error_stack1();
 int32_t bounds_error_stackb();
 int32_t bounds_error_probe();
+int32_t bounds_error_q4();
+int32_t bounds_error_balance();
+int32_t bounds_error_sample();
 int32_t bounds_error_all() {
   int32_t (*const fns[])() = {bounds_error_abi, bounds_error_gemv, bounds_error_grouped, bounds_error_moe,
-                              bounds_error_stack1, bounds_error_stackb, bounds_error_probe};
+                              bounds_error_stack1, bounds_error_stackb, bounds_error_probe,
+                              bounds_error_q4, bounds_error_balance, bounds_error_sample};
   int32_t first = 0;
   for (auto f : fns) {
     const int32_t v = f();

@@ -122,13 +122,14 @@ __device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, in
     const bool live = t < p.T && (!p.mask || p.mask[t] != 0);
 #pragma unroll
     for (int j = 0; j < Tok::kNV; ++j) z[j] = -INFINITY;
-    if (live) Tok::load(z, p.logits + (size_t)t * p.E, p.E);
+    if (live && in_bounds((size_t)t * p.E + p.E - 1, (size_t)p.T * p.E, 30)) Tok::load(z, p.logits + (size_t)t * p.E, p.E);
   };
   // the first token's pairs and logits, on their way while the counts are cleared
   int ids[8];
   bool live = false;
   auto pairs = [&](int t) {
     live = t < p.T && (!p.mask || p.mask[t] != 0);
+    if (live && !in_bounds((size_t)t * p.k + p.k - 1, (size_t)p.T * p.k, 31)) live = false;
     if (p.k % 4 == 0) {
 #pragma unroll
       for (int q = 0; q < 8; q += 4) {
@@ -189,7 +190,8 @@ __device__ __forceinline__ void count_tokens(const BalanceParams &p, int cta, in
     }
 #pragma unroll
     for (int j = 0; j < Tok::kNV / Tok::kTokens; ++j)
-      if (Tok::column(from + j) < p.E) s_w[warp * p.E + Tok::column(from + j)] = acc[j];
+      if (Tok::column(from + j) < p.E && in_bounds(warp * p.E + Tok::column(from + j), (size_t)kWarps * p.E, 32))
+        s_w[warp * p.E + Tok::column(from + j)] = acc[j];
     __syncthreads();
     for (int e = tid; e < p.E; e += THREADS) {
       float q = 0;
@@ -255,7 +257,7 @@ template <class P, class C> __device__ void finish(const BalanceParams &p, Finis
   __syncthreads();
   const int live = s.slice[len];
   const double share = 1. / max(1, live);
-  if (set == 0 && c < len) {
+  if (set == 0 && c < len && in_bounds(e, p.E, 33)) {
     p.counts[e] = n;
     if (p.mean_p) p.mean_p[e] = (float)(q * share);
   }
@@ -290,7 +292,7 @@ template <class P, class C> __device__ void finish(const BalanceParams &p, Finis
         const int y = __shfl_up_sync(0xffffffffu, upto, o);
         if (tid >= o) upto += y;
       }
-      if (i0 + tid < len) p.offsets[e0 + i0 + tid] = b + upto - own;
+      if (i0 + tid < len && in_bounds(e0 + i0 + tid, p.E, 33)) p.offsets[e0 + i0 + tid] = b + upto - own;
       b += __shfl_sync(0xffffffffu, upto, 31);
     }
     if (rank == ctas - 1 && tid == 0) p.offsets[p.E] = b;
@@ -331,6 +333,7 @@ template <class Tok> __global__ void __launch_bounds__(kPartThreads) balance_par
   int32_t *s_c = reinterpret_cast<int32_t *>(s_p + p.E);
   count_tokens<Tok, kPartThreads, double>(p, blockIdx.x, gridDim.x, s_w, s_p, s_c);
   __syncthreads();
+  if (!in_bounds(blockIdx.x, kMaxCtas, 33)) return;
   for (int e = threadIdx.x; e < p.E; e += kPartThreads) p.part_p[(size_t)blockIdx.x * p.E + e] = (float)s_p[e];
   for (int e = threadIdx.x; e <= p.E; e += kPartThreads) p.part_c[(size_t)blockIdx.x * (p.E + 1) + e] = s_c[e];
 }
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kGradThreads)
     const bool live = t < T && (!mask || mask[t] != 0);
 #pragma unroll
     for (int j = 0; j < Tok::kNV; ++j) ahead[j] = -INFINITY;
-    if (live) Tok::load(ahead, logits + (size_t)t * E, E);
+    if (live && in_bounds((size_t)t * E + E - 1, (size_t)T * E, 30)) Tok::load(ahead, logits + (size_t)t * E, E);
   };
   int t = blockIdx.x * kRows + tid / (32 / Tok::kTokens);
   fetch(t);
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(kGradThreads)
     const float by = d == 0.f ? 0.f : scale * r;
 #pragma unroll
     for (int j = 0; j < Tok::kNV; ++j) z[j] = by * z[j] * (f[j] - dot);
-    if (t < T) Tok::store(dlogits + (size_t)t * E, z, E);
+    if (t < T && in_bounds((size_t)t * E + E - 1, (size_t)T * E, 34)) Tok::store(dlogits + (size_t)t * E, z, E);
   }
 }
 
@@ -446,6 +449,8 @@ int32_t check_sizes(int32_t T, int32_t E, int32_t k) {
 }
 
 }  // namespace
+
+NSLM_BOUNDS_ACCESSOR(balance)
 
 size_t balance_ws_bytes(int32_t T, int32_t E) {
   if (T <= kOneLaunchT) return 0;

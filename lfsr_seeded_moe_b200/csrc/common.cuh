@@ -75,7 +75,11 @@ __host__ __device__ inline int32_t ceil_div(int32_t a, int32_t b) { return (a + 
 // Site numbers: 1-2 field copies by offset, 3-4 field loads by row, 5-6 the
 // tensor-core producer's field and token-row loads, 7-9 the tensor-core
 // epilogue's stores, 10-11 the decode kernels' h and y stores, 12 the GEMV's
-// y store, 99 the self-test probe.
+// y store, 20-26 the 4-bit GEMV (weights, scales, their places in the ring,
+// activations, their places, the groups' sums of them, y), 30-34 the balance
+// loss and its gradient (logits, ids, the warps' sums, outputs, dlogits), 40-47
+// sampling (logits, a row's shared copy, the ring, lists, their buckets and
+// order, bins, outputs), 99 the self-test probe.
 #ifndef NSLM_BOUNDS_CHECK
 #define NSLM_BOUNDS_CHECK 0
 #endif
@@ -107,6 +111,11 @@ __device__ __forceinline__ bool in_bounds(size_t idx, size_t n, int site) {
   (void)site;
 #endif
   return true;
+}
+// True when the `bytes` at `at` lie in the `size` bytes from `from` on.
+__device__ __forceinline__ bool in_buffer(const void *at, size_t bytes, const void *from, size_t size, int site) {
+  const size_t off = (size_t)((const char *)at - (const char *)from);
+  return in_bounds(off, size, site) && in_bounds(off + bytes - 1, size, site);
 }
 
 int32_t bounds_error_all();  // the first recorded site over all translation units (and clears them)

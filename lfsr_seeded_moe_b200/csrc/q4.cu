@@ -171,18 +171,24 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
   const uint32_t scales = ring + STAGES * kStage;
   const uint32_t dst2 = scales + (lane / 16) * kScales + (lane % 16) * kScaleRow;
   if (l_step < p.steps) rows_of();
+  const auto weights = [&](uint32_t dst, const uint8_t *src) {
+    if (in_buffer(src, 16, p.W.q, (size_t)N * K / 2, 20) && in_bounds(dst - ring + 15, STAGES * kStage, 22)) copy16(dst, src);
+  };
   auto load_stage = [&]() {
     if (l_st > 0) {
       if (l_left > 0) {
-        copy16(dst0 + l_slot, src0);
-        copy16(dst0 + l_slot + 8 * kRow, src1);
+        weights(dst0 + l_slot, src0);
+        weights(dst0 + l_slot + 8 * kRow, src1);
       }
       if (l_left > 128) {
-        copy16(dst1 + l_slot, src0 + 64);
-        copy16(dst1 + l_slot + 8 * kRow, src1 + 64);
+        weights(dst1 + l_slot, src0 + 64);
+        weights(dst1 + l_slot + 8 * kRow, src1 + 64);
       }
       if (((nst - l_st) & last) == 0) {
-        if (AFFINE || lane < 16) {
+        const int bytes = 2 * (last ? 8 : min(kGps, NG - l_group));  // of the row's scales
+        if ((AFFINE || lane < 16) &&
+            in_buffer(src2, bytes, AFFINE && lane >= 16 ? p.W.biases : p.W.scales, (size_t)N * NG * 2, 21) &&
+            in_bounds(dst2 + l_chunk - scales + kScaleRow - 1, STAGES * kChunk, 22)) {
           if (last) {
             copy16(dst2 + l_chunk, src2);
           } else if (whole) {
@@ -226,10 +232,13 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
   for (int m = 0; m < MP; ++m)
   for (int w = tid; w < K / 8; w += WARPS * 32) {
     const int gi = w / (G / 8), wi = w % (G / 8);
-    const uint4 v = m < M ? __ldg(reinterpret_cast<const uint4 *>(p.x) + (size_t)m * (K / 8) + w) : make_uint4(0, 0, 0, 0);
+    const uint4 v = m < M && in_bounds((size_t)m * (K / 8) + w, (size_t)M * K / 8, 23)
+                        ? __ldg(reinterpret_cast<const uint4 *>(p.x) + (size_t)m * (K / 8) + w)
+                        : make_uint4(0, 0, 0, 0);
     const uint4 q = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-    xs[((size_t)(gi * kWords + wi % kWords) * MP + m) * 4 + wi / kWords] = q;
+    const size_t place = ((size_t)(gi * kWords + wi % kWords) * MP + m) * 4 + wi / kWords;
+    if (in_bounds(place, (size_t)MP * K / 8, 24)) xs[place] = q;
     if (AFFINE) {
       float s = 0.f;
       const uint32_t h[4] = {v.x, v.y, v.z, v.w};
@@ -244,6 +253,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
         uint16_t *at = sx + m * sx_row + gi / kGps * kSums<G> + gi % kGps;
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
+          if (!in_bounds((size_t)(at - sx) + j * MP * sx_row + kGps, (size_t)3 * MP * sx_row, 25)) break;
           const __nv_bfloat16 b = __float2bfloat16_rn(s);
           at[j * MP * sx_row] = __bfloat16_as_ushort(b);
           at[j * MP * sx_row + kGps] = __bfloat16_as_ushort(__float2bfloat16_rn(8.f * __bfloat162float(b)));
@@ -258,6 +268,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
   const uint32_t xb = smem_addr(smem) + (g < MP ? kZero + ((st0 * (kStageK / 32) * MP + g) * 4 + t) * 16 : 0);
   const uint32_t x_stage = g < MP ? kGps * kWords * MP * 64 : 0;
   const uint32_t sb = smem_addr(sx) + (g < MP ? (g * sx_row + st0 * kSums<G> + 2 * t) * 2 : 0);
+  auto in_sums = [&](uint32_t at) { return in_bounds(at - smem_addr(sx) + 3, (size_t)6 * MP * sx_row, 25); };
   // where the lane's pair of [b s] of row g stands
   const uint32_t co = scales + g * kScaleRow +
                       (kGps == 8 || t < kGps / 2 ? kScales + t * 4 : (t - kGps / 2) * 4);
@@ -288,14 +299,15 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
           for (int j = 0; j < 3; ++j) {
             const uint32_t from = sb + (j * MP * sx_row + st * kSums<G>) * 2;
             uint32_t b0 = 0, b1 = 0;
-            if (g < MP) b0 = lds32(from), b1 = lds32(from + 16);
+            if (g < MP && in_sums(from + 16)) b0 = lds32(from), b1 = lds32(from + 16);
             mma_bf16(c_co, a0, a1, a2, a3, b0, b1);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 3; ++j) {
+            const uint32_t from = sb + (j * MP * sx_row + st * kSums<G>) * 2;
             uint32_t b0 = 0;
-            if (g < MP) b0 = lds32(sb + (j * MP * sx_row + st * kSums<G>) * 2);
+            if (g < MP && in_sums(from)) b0 = lds32(from);
             mma_bf16_k8(c_co, a0, a1, b0);
           }
         }
@@ -309,7 +321,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
         float c[4] = {};
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-          const uint4 b = lds128(xp + (gi * kWords + i) * MP * 64);
+          const uint32_t from = xp + (gi * kWords + i) * MP * 64;
+          const bool staged = in_bounds(from - smem_addr(smem) + 15, kZero + (size_t)2 * MP * K, 24);
+          const uint4 b = staged ? lds128(from) : make_uint4(0, 0, 0, 0);
           mma_bf16(c, pair_of<0>(a0[i]), pair_of<0>(a1[i]), pair_of<1>(a0[i]), pair_of<1>(a1[i]), b.x, b.y);
           mma_bf16(c, pair_of<2>(a0[i]), pair_of<2>(a1[i]), pair_of<3>(a0[i]), pair_of<3>(a1[i]), b.z, b.w);
         }
@@ -343,7 +357,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1) q4_gemv_kernel
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(p.kw * 32) : "memory");
     for (int i = kp * 32 + lane; i < MP * kTile; i += p.kw * 32) {
       const int m = i / kTile, row = (step * tps + sub) * kTile + i % kTile;
-      if (m >= M || row >= N) continue;
+      if (m >= M || row >= N || !in_bounds((size_t)m * N + row, (size_t)M * N, 26)) continue;
       float s = 0.f;
       for (int k = 0; k < p.kw; ++k) s += rb[k * kMaxVec * kTile + i];
       p.y[(size_t)m * N + row] = s;
@@ -445,6 +459,9 @@ int32_t launch_q4(const Q4Params &p, cudaStream_t s) {
 }
 
 }  // namespace
+
+NSLM_BOUNDS_ACCESSOR(q4)
+
 }  // namespace nslm
 
 using namespace nslm;

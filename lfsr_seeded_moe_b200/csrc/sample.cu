@@ -179,7 +179,8 @@ __device__ __forceinline__ void sort_list(Shared &s, int n, float top, float sca
       place += (uint32_t)k > (uint32_t)key;
     }
     order = warp_sum_of<8>(place << 16 | order);
-    if (c < n && (tid & 7) == 0) s.mine[order & 0xffff] = key, s.place[order & 0xffff] = (uint16_t)(order >> 16);
+    if (c < n && (tid & 7) == 0 && in_bounds(order & 0xffff, n, 45))
+      s.mine[order & 0xffff] = key, s.place[order & 0xffff] = (uint16_t)(order >> 16);
     __syncthreads();
     return;
   }
@@ -195,6 +196,7 @@ __device__ __forceinline__ void sort_list(Shared &s, int n, float top, float sca
     x[q] = s.list[tid + q * kThreads];
     by_logit[q] = max(0, min(kThreads - 1, (int)((top - logit_of(x[q])) * scale)));
     by_index[q] = index_of(x[q]) >> shift;
+    if (!in_bounds(by_index[q], kThreads, 44)) by_index[q] = 0;
     at[q] = atomicAdd(&s.start[by_logit[q]], 1u) & 0xffff;
     at[q] |= atomicAdd(&s.start[by_index[q]], 0x10000u) & 0xffff0000u;
   }
@@ -210,8 +212,9 @@ __device__ __forceinline__ void sort_list(Shared &s, int n, float top, float sca
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     if (tid + q * kThreads >= n) break;
-    s.key[(s.start[by_logit[q]] + at[q]) & 0xffff] = x[q];
-    s.low[(s.start[by_index[q]] + (at[q] & 0xffff0000u)) >> 16] = (uint32_t)x[q];
+    const uint32_t to = (s.start[by_logit[q]] + at[q]) & 0xffff, to_low = (s.start[by_index[q]] + (at[q] & 0xffff0000u)) >> 16;
+    if (in_bounds(to, n, 44)) s.key[to] = x[q];
+    if (in_bounds(to_low, n, 44)) s.low[to_low] = (uint32_t)x[q];
   }
   __syncthreads();
 #pragma unroll
@@ -222,6 +225,7 @@ __device__ __forceinline__ void sort_list(Shared &s, int n, float top, float sca
     int order = logit0, place = index0;
     for (int j = logit0; j < logit1; ++j) order += s.key[j] > x[q];
     for (int j = index0; j < index1; ++j) place += s.low[j] > (uint32_t)x[q];  // these fall with the index
+    if (!in_bounds(order, n, 45)) continue;
     s.mine[order] = x[q];
     s.place[order] = (uint16_t)place;
   }
@@ -324,6 +328,7 @@ __device__ __forceinline__ bool draw_from_list(Shared &s, const SampleParams &p,
   for (int q = 0; q < 2; ++q) {
     if (at + q >= t.n) break;
     const int place = s.place[at + q];
+    if (!in_bounds(place, t.n, 45)) continue;
     s.mine[place] = x[q];
     s.key[place] = stays[q] && before + (q ? m[0] : 0) < need ? m[q] : 0;
   }
@@ -333,6 +338,7 @@ __device__ __forceinline__ bool draw_from_list(Shared &s, const SampleParams &p,
   const uint64_t below = sum_before(s, m[0] + m[1], warps, Z), to = target_of(t.u, Z);
   if (below <= to && to < below + m[0] + m[1]) {
     const uint64_t y = s.mine[at + (to < below + m[0] ? 0 : 1)];
+    if (!in_bounds(index_of(y), p.V, 47)) return true;
     p.token[row] = index_of(y);
     if (p.prob) p.prob[row] = (float)(t.weight(logit_of(y)) / (double)Z);
   }
@@ -400,6 +406,12 @@ template <class T, bool RES> struct Row {
   float last_v = -INFINITY;
   int last_i = kMaxV;
 
+  // the CTA's logits, and the up to 15 bytes between an aligned address and them
+  __device__ __forceinline__ bool in_row(const char *at, int bytes) const {
+    const char *lo = (const char *)((uintptr_t)src & ~(uintptr_t)15);
+    return in_buffer(at, bytes, lo, (const char *)(src + n) - lo, 40);
+  }
+
   __device__ __forceinline__ bool kept(int i, float v) const {
     return v > last_v || (v == last_v && first + i <= last_i);
   }
@@ -410,7 +422,10 @@ template <class T, bool RES> struct Row {
   __device__ __forceinline__ float value(float v) const {
     return infinite ? (v == INFINITY ? 0.f : -INFINITY) : v;
   }
-  __device__ __forceinline__ float at(int i) const { return RES ? l[i] : value(logit_of(src[i])); }
+  __device__ __forceinline__ float at(int i) const {
+    if (!in_bounds(i, n, RES ? 41 : 40)) return -INFINITY;
+    return RES ? l[i] : value(logit_of(src[i]));
+  }
 
   // f(i, logit) for this thread's logits, U at a time so that their latencies overlap.
   template <int U, class F> __device__ __forceinline__ void each(F f) const {
@@ -440,7 +455,9 @@ template <class T, bool RES> struct Row {
 #pragma unroll
         for (int j = 0; j < kRingChunk; j += 512) {
           const int off = c * kRingChunk + j + lane * 16;
-          if (off < bytes)
+          if (off < bytes && in_row(from + off, min(16, bytes - off)) &&
+              in_bounds(warp * kRing * kRingChunk + c % kRing * kRingChunk + j + lane * 16 + 15,
+                        kWarps * kRing * kRingChunk, 42))
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + c % kRing * kRingChunk + j),
                          "l"(from + off), "r"(min(16, bytes - off))
                          : "memory");
@@ -611,7 +628,7 @@ template <class T, bool RES> struct Row {
       int c = i, k = 0;
       while (c >= (int)counts[k]) c -= (int)counts[k++];
       const Shared *o = ctas == 1 ? &s : cg::this_cluster().map_shared_rank(&s, k);
-      s.list[i] = o->mine[c];
+      if (in_bounds(k, ctas, 43) && in_bounds(c, kList, 43)) s.list[i] = o->mine[c];
     }
     __syncthreads();
     return total;
@@ -631,6 +648,7 @@ template <class T, bool RES> struct Row {
       auto count = [&](auto even, int i, float v) {
         if (!inside(i, v)) return;
         const int b = r.template bin_as<decltype(even)::value>(v);
+        if (!in_bounds((uint32_t)b, kBins, 46)) return;
         if (by_mass) {
           const uint64_t x = w.fixed(v);
           const uint32_t lo = (uint32_t)x, old = atomicAdd(&s.hist.lo[b], lo);
@@ -757,7 +775,7 @@ template <class T, bool RES> __device__ __noinline__ float list_start(Row<T, RES
   const float scale = __fdividef(kCountBins, 8.f * temp);
   r.template each<4>([&](int, float v) {
     const int b = (int)((from - v) * scale);
-    if (b < kCountBins) atomicAdd(&r.s.count[max(0, b)], 1u);
+    if (b < kCountBins && in_bounds(max(0, b), kCountBins, 46)) atomicAdd(&r.s.count[max(0, b)], 1u);
   });
   if (tid == 0) r.s.found = -1;
   r.sync_row();
@@ -794,6 +812,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   const T *src = reinterpret_cast<const T *>(p.logits) + (size_t)row * p.ld + first;
   float *l = reinterpret_cast<float *>(&s + 1);
+  // the CTA's part lies in its row, and a logit's place in the shared copy
+  auto inside = [&](int i, int many) {
+    return in_bounds((size_t)i + many - 1, n, 40) && in_bounds((size_t)first + i + many - 1, p.V, 40) &&
+           in_bounds((size_t)(l - reinterpret_cast<float *>(&s + 1)) + i + many - 1, p.len + 8, 41);
+  };
   float hi = -INFINITY;
   if constexpr (RES) {
     // 16-byte loads from the first aligned address on; the shared copy is
@@ -809,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int vecs = n < kThreads * kVec ? 0 : (n - head) / kVec;
 #pragma unroll 4
     for (int i = tid; i < vecs; i += kThreads) {
+      if (!inside(head + i * kVec, kVec)) break;
       const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(src + head) + i);
       float4 *dst = reinterpret_cast<float4 *>(l + head) + i * (kVec / 4);
       const uint32_t x[4] = {q.x, q.y, q.z, q.w};
@@ -825,9 +849,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < kVec; j += 4) dst[j / 4] = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
     }
-    if (tid < head) l[tid] = put(logit_of(src[tid]));
+    if (tid < head && inside(tid, 1)) l[tid] = put(logit_of(src[tid]));
 #pragma unroll 4
-    for (int i = head + vecs * kVec + tid; i < n; i += kThreads) l[i] = put(logit_of(src[i]));
+    for (int i = head + vecs * kVec + tid; i < n; i += kThreads)
+      if (inside(i, 1)) l[i] = put(logit_of(src[i]));
   }
   Row<T, RES> r{s, l, src, n, first, rank, ctas, tid >> 5, tid & 31};
   static_assert(kThreads == 512);
@@ -881,6 +906,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int o = 16; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   auto put_out = [&](int token, float prob) {
+    if (!in_bounds(token + 1, p.V + 1, 47)) return;  // -1: nothing left
     p.token[row] = token;
     if (p.prob) p.prob[row] = prob;
   };
@@ -1033,6 +1059,9 @@ template <class T> int32_t launch_sample(SampleParams p, int32_t B, cudaStream_t
 }
 
 }  // namespace
+
+NSLM_BOUNDS_ACCESSOR(sample)
+
 }  // namespace nslm
 
 using namespace nslm;
