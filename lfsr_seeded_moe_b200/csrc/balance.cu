@@ -98,7 +98,7 @@ template <int LANES, int NV, bool VEC> struct Token {
 };
 
 // One pass over the logits with the running sums in registers.  65536 tokens of
-// 128 experts take 13.3 us in two launches, 3 of them the second and its wait;
+// 128 experts take 13.4 us in two launches, 3 of them the second and its wait;
 // the logits' 32 MB take 4.9 at the copy rate, and the exponentials, shuffles
 // and the ids' shared-memory atomics are the rest.  64 tokens of 100 experts
 // take 4.1 us, all latency.

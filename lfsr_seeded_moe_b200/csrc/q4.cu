@@ -35,11 +35,12 @@ __device__ __forceinline__ float bf16_f32(uint32_t h) { return __uint_as_float(h
 // over the groups, [b s] times [x's sum, 8 times that], with b and s as they are
 // stored (bf16) and the sums in three bf16 parts (24 bits): 3 mma a stage.
 //
-// 131072 x 4096 with groups of 64 takes 65 us with one vector and 68 with 8 (306
-// MB: 47 at the copy rate; 75 to 80 in runs of thousands), 50257 x 2048 15.5 (8.8).  Copies alone take
-// 48 to 55 us of the first, computing alone 52 to 62 (the unpacking's shifts and
-// masks on the ALU pipe), and they overlap but for the rest.  512 x 1024 takes
-// 2 us, a launch and a load.
+// 131072 x 4096 with groups of 64 takes 64 to 66 us with one vector and 68 to 76
+// with 8 in bursts of 100 calls, 72 and 75 to 80 in runs of thousands (306 MB: 47
+// at the copy rate); 50257 x 2048 15.5 (8.8).  Copies alone take 48 to 55 us of
+// the first, computing alone 52 to 62 (the unpacking's shifts and masks on the
+// ALU pipe), and they overlap but for the rest.  512 x 1024 takes 2 us, a launch
+// and a load.
 
 constexpr int kTile = 16;
 constexpr int kStageK = 256;             // weights of a row in a stage

@@ -54,7 +54,7 @@ struct SampleParams {
 // the same u gives the same token.
 //
 // One row of 32003 logits with top-k 50 and top-p takes 8.1 us, nearly all of it
-// latency: its load, four exchanges, the list's sort and sums; 64 x 131072 without a filter 31 us, bound by the
+// latency: its load, four exchanges, the list's sort and sums; 64 x 131072 without a filter 32 us, bound by the
 // instructions of two passes (0.62 of the issue slots, DRAM at 15%).
 
 // Weights in units of 2^-44.  exp(x) = 2^(k/16) e^r, |r| <= ln 2 / 32, with the
